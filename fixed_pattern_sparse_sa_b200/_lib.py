@@ -24,6 +24,10 @@ EXPORTS = (
     "sa_debug_set_spin_limit", "sa_debug_inject_stall", "sa_debug_exact_recompute_rows",
     "sa_probe_gather",
     "sa_indexer_scores_at", "sa_topk_merge", "sa_index_shard",
+    "sa_sink_attn_fwd", "sa_sink_attn_bwd_workspace_size", "sa_sink_attn_bwd",
+    "sa_paged_attn_decode_workspace_size", "sa_paged_attn_decode",
+    "sa_paged_books_workspace_size", "sa_paged_extend", "sa_paged_write", "sa_paged_fork",
+    "sa_paged_free", "sa_paged_compact",
 )
 
 SA_OK = 0
@@ -47,6 +51,28 @@ class sa_pattern(ctypes.Structure):
 class sa_dsa_layer(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("q", "k", "v", "q_idx", "k_idx", "w", "out", "lse")]
+
+
+SA_BF16, SA_FP16 = 0, 1
+
+
+class sa_sink_shape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("dtype", "B", "Hq", "Hkv", "d", "window", "sinks")] +
+                [("scale", ctypes.c_float)] +
+                [(n, ctypes.c_int64) for n in ("Tq", "L", "q_pos0", "max_q", "max_k")] +
+                [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride", "out_stride", "dout_stride",
+                                                "lse_stride")])
+
+
+class sa_paged_shape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("dtype", "B", "Hq", "Hkv", "d", "page", "max_pages", "window",
+                                               "sinks")] +
+                [("scale", ctypes.c_float), ("n_pages", ctypes.c_int64), ("q_stride", ctypes.c_int64 * 2),
+                 ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3)])
+
+
+class sa_page_cache(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -101,6 +127,17 @@ def load() -> ctypes.CDLL:
             "sa_indexer_scores_at": (I, [P, P, P, I, I, I, I, I, P, I, P, P]),
             "sa_topk_merge": (I, [P, P, P, I, I64, I, I, I, I64, P, P, P]),
             "sa_index_shard": (I, [P, I64, I64, I64, P, P]),
+            "sa_sink_attn_fwd": (I, [P, P, P, P, P, P, P, P, P]),
+            "sa_sink_attn_bwd_workspace_size": (SZ, [P, I]),
+            "sa_sink_attn_bwd": (I, [P, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+            "sa_paged_attn_decode_workspace_size": (SZ, [I, I, I, I]),
+            "sa_paged_attn_decode": (I, [P, P, P, P, P, P, P, P, P, SZ, P]),
+            "sa_paged_books_workspace_size": (SZ, [I, I, I64]),
+            "sa_paged_extend": (I, [P, P, P, I, I, I64, I, P, P, I, P, P, SZ, P]),
+            "sa_paged_write": (I, [P, P, P, P, P, P, P, P, I, I64, I, I, I64, I, I, I, I, P, P, P, P, P]),
+            "sa_paged_fork": (I, [P, P, P, I, I, I64, I, P, P, I, P, I, I64, P, P, SZ, P]),
+            "sa_paged_free": (I, [P, P, P, I, I, I64, I, P, I, I, I, P]),
+            "sa_paged_compact": (I, [P, P, I, I, I64, I, P, I, I64, P, P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)

@@ -30,6 +30,7 @@
 #include "nsa_bwd_tc.cuh"
 #include "probe_gather.cuh"
 
+
 using namespace sa;
 
 // ------------------------------------------------------------- error state --
@@ -2059,3 +2060,5 @@ int sa_index_shard(const int32_t *idx, int64_t n, int64_t key_lo, int64_t key_hi
     SA_CHECK_LAUNCH("index_shard_kernel");
     return SA_OK;
 }
+
+#include "serving_api.cuh"

@@ -1,0 +1,430 @@
+// serving_api.cuh -- C ABI entry points of the sink-window attention, the
+// paged decode attention and the pages of a cache (declared in include/sa.h).
+// Included at the end of sa_api.cu, whose launch, error and alignment helpers
+// it uses.
+#pragma once
+
+#include "paged_attn.cuh"
+#include "paged_books.cuh"
+#include "sink_attn.cuh"
+
+// ---------------------------------------------------- sink-window attention --
+static bool strides_ok(const int64_t *s, int n, long long mul) {
+    for (int i = 0; i < n; ++i)
+        if (s[i] < 0 || s[i] % mul) return false;
+    return true;
+}
+
+static int sink_check(const char *what, const sa_sink_shape *s, const void *q, const void *k, const void *v,
+                      const int32_t *cu_q, const int32_t *cu_k, bool bwd) {
+    if (!s) return fail(SA_ERR_INVALID_ARG, "%s: shape is null", what);
+    if (s->B <= 0 || s->Tq < 0 || s->L < 0 || s->Hq <= 0 || s->Hkv <= 0 || s->Hq % s->Hkv || s->q_pos0 < 0 ||
+        s->max_q < 0 || s->max_k < 0)
+        return fail(SA_ERR_INVALID_ARG, "%s: bad sizes (Hq a multiple of Hkv)", what);
+    if (s->window < 1 || s->sinks < 0) return fail(SA_ERR_INVALID_ARG, "%s: window >= 1, sinks >= 0", what);
+    if (!std::isfinite(s->scale)) return fail(SA_ERR_INVALID_ARG, "%s: scale", what);
+    if (s->d != 64 && s->d != 128) return fail(SA_ERR_UNSUPPORTED, "%s: head dim %d (64 or 128)", what, s->d);
+    if (s->dtype != SA_BF16 && (bwd || s->dtype != SA_FP16))
+        return fail(SA_ERR_UNSUPPORTED, "%s: dtype %d", what, s->dtype);
+    // positions, row numbers and key tiles are 32-bit
+    if (s->Tq >= INT_MAX / 2 || s->L >= INT_MAX / 2 || s->q_pos0 >= INT_MAX / 2)
+        return fail(SA_ERR_UNSUPPORTED, "%s: lengths above 2^30", what);
+    if ((long long)s->B * s->Tq * s->Hq >= (1ll << 40) || (long long)s->B * s->L * s->Hkv >= (1ll << 40))
+        return fail(SA_ERR_UNSUPPORTED, "%s: too many rows", what);
+    if ((cu_q == nullptr) != (cu_k == nullptr)) return fail(SA_ERR_INVALID_ARG, "%s: cu_q and cu_k go together", what);
+    const bool no_q = s->Tq == 0, no_k = s->L == 0;       // an empty tensor may have a null pointer
+    if ((!no_q && (!q || !aligned16(q))) || (!no_k && (!k || !v || !aligned16(k) || !aligned16(v))) ||
+        (cu_q && (!aligned4(cu_q) || !aligned4(cu_k))))
+        return fail(SA_ERR_INVALID_ARG, "%s: null or misaligned pointer", what);
+    if (!strides_ok(s->q_stride, 3, 8) || !strides_ok(s->k_stride, 3, 8) || !strides_ok(s->v_stride, 3, 8))
+        return fail(SA_ERR_INVALID_ARG, "%s: strides must be multiples of 8 elements, not negative", what);
+    return SA_OK;
+}
+
+static SinkParams sink_params(const sa_sink_shape *s, const void *q, const void *k, const void *v,
+                              const int32_t *cu_q, const int32_t *cu_k) {
+    SinkParams p{};
+    p.q = q; p.k = k; p.v = v;
+    for (int i = 0; i < 3; ++i) {
+        p.q_s[i] = s->q_stride[i]; p.k_s[i] = s->k_stride[i]; p.v_s[i] = s->v_stride[i];
+        p.o_s[i] = s->out_stride[i]; p.do_s[i] = s->dout_stride[i]; p.lse_s[i] = s->lse_stride[i];
+    }
+    p.cu_q = cu_q; p.cu_k = cu_k;
+    p.B = s->B; p.Hq = s->Hq; p.Hkv = s->Hkv; p.G = s->Hq / s->Hkv;
+    p.window = s->window; p.sinks = s->sinks;
+    p.Tq = s->Tq; p.L = s->L; p.q_pos0 = s->q_pos0; p.max_q = s->max_q; p.max_k = s->max_k;
+    p.scale = s->scale; p.scale_log2 = s->scale * kLog2e;
+    return p;
+}
+
+static unsigned sink_row_blocks(long long rows) { return (unsigned)std::min<long long>((rows + 3) / 4, 1 << 30); }
+
+template <typename T>
+static int sink_fwd_launch(const SinkParams &p, int d, cudaStream_t st) {
+    const unsigned g = sink_row_blocks((p.cu_q ? 1 : p.B) * p.Tq * p.Hq);
+    if (d == 64) launch_k("sink_fwd_rows_kernel<64>", sink_fwd_rows_kernel<T, 64>, g, 128, 0, st, p);
+    else launch_k("sink_fwd_rows_kernel<128>", sink_fwd_rows_kernel<T, 128>, g, 128, 0, st, p);
+    SA_CHECK_LAUNCH("sink_fwd_rows_kernel");
+    return SA_OK;
+}
+
+extern "C" int sa_sink_attn_fwd(const sa_sink_shape *shape, const void *q, const void *k, const void *v,
+                                const int32_t *cu_q, const int32_t *cu_k, void *out, float *lse, void *stream) {
+    SA_TRACE("sa_sink_attn_fwd");
+    int rc = sink_check("sink_attn_fwd", shape, q, k, v, cu_q, cu_k, false);
+    if (rc) return rc;
+    if (shape->Tq == 0) return SA_OK;
+    if (!out || !lse || !aligned16(out) || !aligned4(lse))
+        return fail(SA_ERR_INVALID_ARG, "sink_attn_fwd: null or misaligned output");
+    SinkParams p = sink_params(shape, q, k, v, cu_q, cu_k);
+    rc = device_error_word(&p.err);
+    if (rc) return rc;
+    p.out = out; p.lse = lse;
+    cudaStream_t st = as_stream(stream);
+    return shape->dtype == SA_BF16 ? sink_fwd_launch<__nv_bfloat16>(p, shape->d, st)
+                                   : sink_fwd_launch<__half>(p, shape->d, st);
+}
+
+extern "C" size_t sa_sink_attn_bwd_workspace_size(const sa_sink_shape *s, int packed) {
+    if (!s || s->B <= 0 || s->Tq < 0 || s->Hq <= 0) return 0;
+    return round_up((size_t)(packed ? 1 : s->B) * s->Tq * s->Hq * 8, 256);
+}
+
+template <int D>
+static int sink_bwd_launch(const SinkParams &p, cudaStream_t st) {
+    using T = __nv_bfloat16;
+    const long long nb = p.cu_q ? 1 : p.B;
+    if (p.Tq > 0) {
+        const unsigned g = sink_row_blocks(nb * p.Tq * p.Hq);
+        launch_k("sink_bwd_prep_kernel", sink_bwd_prep_kernel<T, D>, g, 128, 0, st, p);
+        SA_CHECK_LAUNCH("sink_bwd_prep_kernel");
+        launch_k("sink_dq_rows_kernel", sink_dq_rows_kernel<T, D>, g, 128, 0, st, p);
+        SA_CHECK_LAUNCH("sink_dq_rows_kernel");
+    }
+    if (p.L > 0) {
+        launch_k("sink_dkv_rows_kernel", sink_dkv_rows_kernel<T, D>, sink_row_blocks(nb * p.L * p.Hkv), 128, 0, st, p);
+        SA_CHECK_LAUNCH("sink_dkv_rows_kernel");
+    }
+    return SA_OK;
+}
+
+extern "C" int sa_sink_attn_bwd(const sa_sink_shape *shape, const void *q, const void *k, const void *v,
+                                const void *out, const float *lse, const void *dout, const int32_t *cu_q,
+                                const int32_t *cu_k, void *dq, void *dk, void *dv, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+    SA_TRACE("sa_sink_attn_bwd");
+    int rc = sink_check("sink_attn_bwd", shape, q, k, v, cu_q, cu_k, true);
+    if (rc) return rc;
+    if (!strides_ok(shape->out_stride, 3, 8) || !strides_ok(shape->dout_stride, 3, 8) ||
+        !strides_ok(shape->lse_stride, 3, 1))
+        return fail(SA_ERR_INVALID_ARG, "sink_attn_bwd: strides must be multiples of 8 elements, not negative");
+    if (shape->Tq > 0 && (!out || !lse || !dout || !dq || !aligned16(out) || !aligned4(lse) || !aligned16(dout) ||
+                          !aligned16(dq)))
+        return fail(SA_ERR_INVALID_ARG, "sink_attn_bwd: null or misaligned pointer");
+    if (shape->L > 0 && (!dk || !dv || !aligned16(dk) || !aligned16(dv)))
+        return fail(SA_ERR_INVALID_ARG, "sink_attn_bwd: null or misaligned pointer");
+    const size_t need = sa_sink_attn_bwd_workspace_size(shape, cu_q != nullptr);
+    if (workspace_bytes < need || (need && !workspace))
+        return fail(SA_ERR_WORKSPACE, "sink_attn_bwd: workspace %zu < %zu", workspace_bytes, need);
+    if (!aligned16(workspace)) return fail(SA_ERR_INVALID_ARG, "sink_attn_bwd: workspace alignment");
+    SinkParams p = sink_params(shape, q, k, v, cu_q, cu_k);
+    rc = device_error_word(&p.err);
+    if (rc) return rc;
+    p.o = out; p.lse_in = lse; p.dout = dout;
+    p.dq = dq; p.dk = dk; p.dv = dv; p.stat = static_cast<float2 *>(workspace);
+    cudaStream_t st = as_stream(stream);
+    return shape->d == 64 ? sink_bwd_launch<64>(p, st) : sink_bwd_launch<128>(p, st);
+}
+
+// ------------------------------------------------- paged decode attention --
+template <int D>
+static int pd_grid() { return sm_count() * (D == 64 ? 2 : 1); }   // CTAs that fit with their rings at once
+
+static size_t pd_part_floats(int d) {
+    return (size_t)(d == 64 ? pd_grid<64>() : pd_grid<128>()) * 2 * PD_NW * 16 * (d + 2);
+}
+
+extern "C" size_t sa_paged_attn_decode_workspace_size(int B, int Hq, int Hkv, int d) {
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || (d != 64 && d != 128)) return 0;
+    return round_up((size_t)(B + 1) * 8, 256) + pd_part_floats(d) * 4;
+}
+
+template <typename T, int D>
+static int pd_launch(const PagedParams &p, cudaStream_t st) {
+    const int smem = PdSmem<D>::TOTAL, gx = pd_grid<D>();
+    int rc = set_smem(paged_decode_kernel<T, D>, smem);
+    if (rc) return rc;
+    launch_k("paged_decode_kernel", paged_decode_kernel<T, D>, gx, PD_THREADS, smem, st, p);
+    SA_CHECK_LAUNCH("paged_decode_kernel");
+    const dim3 gj((unsigned)((long long)p.B * p.Hkv * p.HT), (unsigned)((std::min(p.G, 16) + 3) / 4));
+    launch_k("paged_join_kernel", paged_join_kernel<T, D>, gj, 256, 0, st, p, gx);
+    SA_CHECK_LAUNCH("paged_join_kernel");
+    return SA_OK;
+}
+
+extern "C" int sa_paged_attn_decode(const sa_paged_shape *s, const void *q, const void *k_cache, const void *v_cache,
+                                    const int32_t *block_table, const int32_t *seq_lens, void *out, float *lse,
+                                    void *workspace, size_t workspace_bytes, void *stream) {
+    SA_TRACE("sa_paged_attn_decode");
+    if (!s) return fail(SA_ERR_INVALID_ARG, "paged_attn_decode: shape is null");
+    if (s->B < 0 || s->Hq <= 0 || s->Hkv <= 0 || s->Hq % s->Hkv || s->page <= 0 || s->max_pages < 0 || s->n_pages < 0 ||
+        s->window < 0 || s->sinks < 0)
+        return fail(SA_ERR_INVALID_ARG, "paged_attn_decode: bad sizes (Hq a multiple of Hkv)");
+    if (!std::isfinite(s->scale)) return fail(SA_ERR_INVALID_ARG, "paged_attn_decode: scale");
+    if (s->d != 64 && s->d != 128) return fail(SA_ERR_UNSUPPORTED, "paged_attn_decode: head dim %d (64 or 128)", s->d);
+    if (s->dtype != SA_BF16 && s->dtype != SA_FP16)
+        return fail(SA_ERR_UNSUPPORTED, "paged_attn_decode: dtype %d", s->dtype);
+    if ((long long)s->max_pages * s->page >= INT_MAX / 2)
+        return fail(SA_ERR_UNSUPPORTED, "paged_attn_decode: %d pages of %d tokens (below 2^30 tokens)", s->max_pages,
+                    s->page);
+    if ((long long)s->B * s->Hq >= INT_MAX / 2 || s->n_pages > INT_MAX)
+        return fail(SA_ERR_UNSUPPORTED, "paged_attn_decode: too many rows or pages");
+    if (s->B == 0) return SA_OK;
+    const bool no_kv = s->n_pages == 0 || s->max_pages == 0;      // an empty pool may have null pointers
+    if (!q || !seq_lens || !out || !lse || !aligned16(q) || !aligned4(seq_lens) || !aligned16(out) || !aligned4(lse) ||
+        (!no_kv && (!k_cache || !v_cache || !block_table)) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !aligned4(block_table))
+        return fail(SA_ERR_INVALID_ARG, "paged_attn_decode: null or misaligned pointer");
+    if (!strides_ok(s->q_stride, 2, 8) || !strides_ok(s->k_stride, 3, 8) || !strides_ok(s->v_stride, 3, 8))
+        return fail(SA_ERR_INVALID_ARG, "paged_attn_decode: strides must be multiples of 8 elements, not negative");
+    const size_t need = sa_paged_attn_decode_workspace_size(s->B, s->Hq, s->Hkv, s->d);
+    if (!workspace || workspace_bytes < need)
+        return fail(SA_ERR_WORKSPACE, "paged_attn_decode: workspace %zu < %zu", workspace_bytes, need);
+    if (!aligned16(workspace)) return fail(SA_ERR_INVALID_ARG, "paged_attn_decode: workspace alignment");
+    PagedParams p{};
+    int rc = device_error_word(&p.err);
+    if (rc) return rc;
+    p.q = q; p.k = k_cache; p.v = v_cache;
+    for (int i = 0; i < 2; ++i) p.q_s[i] = s->q_stride[i];
+    for (int i = 0; i < 3; ++i) { p.k_s[i] = s->k_stride[i]; p.v_s[i] = s->v_stride[i]; }
+    p.table = block_table; p.lens = seq_lens;
+    p.B = s->B; p.Hq = s->Hq; p.Hkv = s->Hkv; p.G = s->Hq / s->Hkv; p.HT = (p.G + 15) / 16;
+    p.page = s->page; p.max_pages = no_kv ? 0 : s->max_pages; p.window = s->window; p.sinks = s->sinks;
+    p.n_pages = s->n_pages; p.scale_log2 = s->scale * kLog2e;
+    p.out = out; p.lse = lse;
+    p.c0 = static_cast<long long *>(workspace);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + round_up((size_t)(s->B + 1) * 8, 256));
+    cudaStream_t st = as_stream(stream);
+    if (s->dtype == SA_BF16)
+        return s->d == 64 ? pd_launch<__nv_bfloat16, 64>(p, st) : pd_launch<__nv_bfloat16, 128>(p, st);
+    return s->d == 64 ? pd_launch<__half, 64>(p, st) : pd_launch<__half, 128>(p, st);
+}
+
+// --------------------------------------------------------- pages of a cache --
+struct BooksLayout {
+    size_t owner, mark, ends, seq, from, to, moves, map, total;
+};
+static BooksLayout books_layout(int S, int n, int64_t n_pages) {
+    BooksLayout l{};
+    size_t at = 0;
+    auto take = [&](size_t ints) { const size_t o = at; at += round_up(ints * 4, 256); return o; };
+    l.owner = take(S); l.mark = take(S);
+    l.ends = take(n); l.seq = take(n);
+    const size_t moves = std::max<size_t>(n, n_pages);
+    l.from = take(moves); l.to = take(moves);
+    l.moves = take(2); l.map = take(n_pages);
+    l.total = at;
+    return l;
+}
+
+extern "C" size_t sa_paged_books_workspace_size(int S, int n, int64_t n_pages) {
+    if (S < 0 || n < 0 || n_pages < 0) return 0;
+    return books_layout(S, n, n_pages).total;
+}
+
+static int books_check(const char *what, const void *table, const void *lens, const void *refcount, int S,
+                       int max_pages, int64_t n_pages, int page, int n) {
+    if (S < 0 || max_pages < 0 || n_pages < 0 || page <= 0 || n < 0)
+        return fail(SA_ERR_INVALID_ARG, "%s: bad sizes", what);
+    if (n_pages >= INT_MAX || max_pages >= (1 << 26) || (long long)max_pages * page >= INT_MAX / 2)
+        return fail(SA_ERR_UNSUPPORTED, "%s: %d pages of %d tokens per sequence, %lld in all (below 2^30 tokens)", what,
+                    max_pages, page, (long long)n_pages);
+    if ((S > 0 && (!lens || (max_pages > 0 && !table))) || (n_pages > 0 && !refcount) || !aligned4(table) ||
+        !aligned4(lens) || !aligned4(refcount))
+        return fail(SA_ERR_INVALID_ARG, "%s: null or misaligned pointer", what);
+    return SA_OK;
+}
+
+static int books_params(const char *what, BooksParams &p, int32_t *table, int32_t *lens, int32_t *refcount, int S,
+                        int max_pages, int64_t n_pages, int page, const int32_t *a, const int32_t *c, int n,
+                        int32_t *result, void *ws, size_t ws_bytes) {
+    const BooksLayout l = books_layout(S, n, n_pages);
+    if (ws_bytes < l.total || (l.total && !ws))
+        return fail(SA_ERR_WORKSPACE, "%s: workspace %zu < %zu", what, ws_bytes, l.total);
+    if (!aligned16(ws)) return fail(SA_ERR_INVALID_ARG, "%s: workspace alignment", what);
+    char *w = static_cast<char *>(ws);
+    auto at = [&](size_t o) { return reinterpret_cast<int32_t *>(w + o); };
+    p.table = table; p.lens = lens; p.refcount = refcount;
+    p.S = S; p.max_pages = max_pages; p.page = page; p.n_pages = n_pages;
+    p.a = a; p.c = c; p.n = n; p.result = result;
+    p.owner = at(l.owner); p.srcmark = at(l.mark); p.ends = at(l.ends); p.seq = at(l.seq);
+    p.from = at(l.from); p.to = at(l.to); p.n_moves = at(l.moves); p.map = at(l.map);
+    return device_error_word(&p.err);
+}
+
+// Checks the caches; vec: bytes of the widest vector that all of them allow.
+static int caches_check(const char *what, const sa_page_cache *caches, int n_caches, int64_t slot_bytes, int &vec) {
+    if (n_caches < 0 || slot_bytes < 0 || (n_caches > 0 && !caches))
+        return fail(SA_ERR_INVALID_ARG, "%s: bad caches", what);
+    vec = slot_bytes % 16 ? 4 : 16;
+    if (n_caches > 0 && slot_bytes % 4) return fail(SA_ERR_UNSUPPORTED, "%s: slots of %lld bytes (a multiple of 4)", what,
+                                                    (long long)slot_bytes);
+    for (int i = 0; i < n_caches; ++i) {
+        const sa_page_cache &c = caches[i];
+        if (!c.base || c.page_stride < 0 || c.slot_stride < 0)
+            return fail(SA_ERR_INVALID_ARG, "%s: cache %d", what, i);
+        const unsigned long long bits = reinterpret_cast<uintptr_t>(c.base) | (unsigned long long)c.page_stride |
+                                        (unsigned long long)c.slot_stride;
+        if (bits % 4) return fail(SA_ERR_INVALID_ARG, "%s: cache %d is not aligned to 4 bytes", what, i);
+        if (bits % 16) vec = 4;
+    }
+    return SA_OK;
+}
+
+static int copy_pages(const BooksParams &b, const sa_page_cache *caches, int n_caches, int64_t slot_bytes, int vec,
+                      bool compact, cudaStream_t st) {
+    bool remap = compact;
+    for (int c0 = 0; c0 < n_caches || remap; c0 += PC_MAX_CACHES) {
+        CopyParams p{};
+        p.from = b.from; p.to = b.to; p.n = b.n; p.n_moves = compact ? b.n_moves : nullptr;
+        p.n_caches = std::max(0, std::min(n_caches - c0, PC_MAX_CACHES));
+        bool whole = true;                            // pages are contiguous in every cache
+        for (int i = 0; i < p.n_caches; ++i) {
+            const sa_page_cache &c = caches[c0 + i];
+            p.caches[i] = PageCache{static_cast<char *>(c.base), c.page_stride, c.slot_stride};
+            whole = whole && c.slot_stride == slot_bytes;
+        }
+        p.slots = whole ? 1 : b.page;
+        p.slot_bytes = whole ? slot_bytes * b.page : slot_bytes;
+        if (p.slot_bytes == 0) p.n_caches = 0;
+        if (remap) {
+            p.map = b.map; p.n_live = b.result; p.table = b.table; p.table_n = (long long)b.S * b.max_pages;
+            p.n_pages = b.n_pages; p.err = b.err;
+        }
+        remap = false;
+        const unsigned grid = (unsigned)sm_count() * 4;
+        if (vec == 16) launch_k("paged_copy_kernel<16>", paged_copy_kernel<uint4>, grid, 256, 0, st, p);
+        else launch_k("paged_copy_kernel<4>", paged_copy_kernel<uint32_t>, grid, 256, 0, st, p);
+        SA_CHECK_LAUNCH("paged_copy_kernel");
+    }
+    return SA_OK;
+}
+
+extern "C" int sa_paged_extend(int32_t *block_table, int32_t *seq_lens, int32_t *refcount, int S, int max_pages,
+                               int64_t n_pages, int page, const int32_t *seqs, const int32_t *n_new, int n,
+                               int32_t *start, void *workspace, size_t workspace_bytes, void *stream) {
+    SA_TRACE("sa_paged_extend");
+    int rc = books_check("paged_extend", block_table, seq_lens, refcount, S, max_pages, n_pages, page, n);
+    if (rc) return rc;
+    if (n == 0) return SA_OK;
+    if (!seqs || !n_new || !start || !aligned4(seqs) || !aligned4(n_new) || !aligned4(start))
+        return fail(SA_ERR_INVALID_ARG, "paged_extend: null or misaligned pointer");
+    BooksParams p{};
+    rc = books_params("paged_extend", p, block_table, seq_lens, refcount, S, max_pages, n_pages, page, seqs, n_new, n,
+                      start, workspace, workspace_bytes);
+    if (rc) return rc;
+    launch_k("paged_extend_kernel", paged_extend_kernel, PB_CTAS, PB_THREADS, 0, as_stream(stream), p);
+    SA_CHECK_LAUNCH("paged_extend_kernel");
+    return SA_OK;
+}
+
+extern "C" int sa_paged_write(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                              const int32_t *block_table, const int32_t *seqs, const int32_t *start,
+                              const int32_t *cu_new, int n, int64_t N, int S, int max_pages, int64_t n_pages, int page,
+                              int Hkv, int d, int elem_bytes, const int64_t *k_new_stride, const int64_t *v_new_stride,
+                              const int64_t *k_stride, const int64_t *v_stride, void *stream) {
+    SA_TRACE("sa_paged_write");
+    if (n < 0 || N < 0 || S < 0 || max_pages < 0 || n_pages < 0 || page <= 0 || Hkv <= 0 || d <= 0 || elem_bytes <= 0 ||
+        !k_new_stride || !v_new_stride || !k_stride || !v_stride || (!cu_new && N != n))
+        return fail(SA_ERR_INVALID_ARG, "paged_write: bad sizes (without cu_new one row per entry)");
+    if ((long long)d * elem_bytes % 16 || (long long)Hkv * d * elem_bytes >= (1 << 28))
+        return fail(SA_ERR_UNSUPPORTED, "paged_write: rows of %lld bytes (a multiple of 16)", (long long)d * elem_bytes);
+    if (n == 0 || N == 0) return SA_OK;
+    if (!k_new || !v_new || !seqs || !start || !aligned16(k_new) || !aligned16(v_new) || !aligned4(seqs) ||
+        !aligned4(start) || !aligned4(cu_new) || !aligned4(block_table) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        (S > 0 && max_pages > 0 && !block_table) || (n_pages > 0 && (!k_cache || !v_cache)))
+        return fail(SA_ERR_INVALID_ARG, "paged_write: null or misaligned pointer");
+    PagedWriteParams p{};
+    const void *src[2] = {k_new, v_new};
+    void *dst[2] = {k_cache, v_cache};
+    const int64_t *ss[2] = {k_new_stride, v_new_stride}, *ds[2] = {k_stride, v_stride};
+    for (int i = 0; i < 2; ++i) {
+        p.src[i] = static_cast<const char *>(src[i]);
+        p.dst[i] = static_cast<char *>(dst[i]);
+        for (int j = 0; j < 2; ++j) p.src_s[i][j] = ss[i][j] * elem_bytes;
+        for (int j = 0; j < 3; ++j) p.dst_s[i][j] = ds[i][j] * elem_bytes;
+        for (int j = 0; j < 3; ++j)
+            if (p.dst_s[i][j] < 0 || p.dst_s[i][j] % 16 || (j < 2 && (p.src_s[i][j] < 0 || p.src_s[i][j] % 16)))
+                return fail(SA_ERR_INVALID_ARG, "paged_write: strides must be multiples of 16 bytes, not negative");
+    }
+    int rc = device_error_word(&p.err);
+    if (rc) return rc;
+    p.table = block_table; p.seqs = seqs; p.start = start; p.cu = cu_new;
+    p.n = n; p.S = S; p.max_pages = max_pages; p.page = page; p.Hkv = Hkv; p.row_bytes = d * elem_bytes;
+    p.N = N; p.n_pages = n_pages;
+    const unsigned grid = (unsigned)std::min<long long>((N + 7) / 8, sm_count() * 8);
+    launch_k("paged_write_kernel", paged_write_kernel, grid, 256, 0, as_stream(stream), p);
+    SA_CHECK_LAUNCH("paged_write_kernel");
+    return SA_OK;
+}
+
+extern "C" int sa_paged_fork(int32_t *block_table, int32_t *seq_lens, int32_t *refcount, int S, int max_pages,
+                             int64_t n_pages, int page, const int32_t *src, const int32_t *dst, int n,
+                             const sa_page_cache *caches, int n_caches, int64_t slot_bytes, int32_t *done,
+                             void *workspace, size_t workspace_bytes, void *stream) {
+    SA_TRACE("sa_paged_fork");
+    int rc = books_check("paged_fork", block_table, seq_lens, refcount, S, max_pages, n_pages, page, n), vec = 16;
+    if (rc == SA_OK) rc = caches_check("paged_fork", caches, n_caches, slot_bytes, vec);
+    if (rc) return rc;
+    if (n == 0) return SA_OK;
+    if (!src || !dst || !done || !aligned4(src) || !aligned4(dst) || !aligned4(done))
+        return fail(SA_ERR_INVALID_ARG, "paged_fork: null or misaligned pointer");
+    BooksParams p{};
+    rc = books_params("paged_fork", p, block_table, seq_lens, refcount, S, max_pages, n_pages, page, src, dst, n, done,
+                      workspace, workspace_bytes);
+    if (rc) return rc;
+    cudaStream_t st = as_stream(stream);
+    launch_k("paged_fork_kernel", paged_fork_kernel, PB_CTAS, PB_THREADS, 0, st, p);
+    SA_CHECK_LAUNCH("paged_fork_kernel");
+    return copy_pages(p, caches, n_caches, slot_bytes, vec, false, st);
+}
+
+extern "C" int sa_paged_free(int32_t *block_table, int32_t *seq_lens, int32_t *refcount, int S, int max_pages,
+                             int64_t n_pages, int page, const int32_t *seqs, int n, int window, int sinks,
+                             void *stream) {
+    SA_TRACE("sa_paged_free");
+    if (window < 0 || sinks < 0) return fail(SA_ERR_INVALID_ARG, "paged_free: window and sinks >= 0");
+    int rc = books_check("paged_free", block_table, seq_lens, refcount, S, max_pages, n_pages, page, n);
+    if (rc) return rc;
+    if (n == 0) return SA_OK;
+    if (!seqs || !aligned4(seqs)) return fail(SA_ERR_INVALID_ARG, "paged_free: null or misaligned pointer");
+    BooksParams p{};
+    rc = device_error_word(&p.err);
+    if (rc) return rc;
+    p.table = block_table; p.lens = seq_lens; p.refcount = refcount;
+    p.S = S; p.max_pages = max_pages; p.page = page; p.n_pages = n_pages; p.a = seqs; p.n = n;
+    const unsigned grid = (unsigned)std::min((n + 7) / 8, sm_count() * 8);
+    launch_k("paged_free_kernel", paged_free_kernel, grid, 256, 0, as_stream(stream), p, window, sinks);
+    SA_CHECK_LAUNCH("paged_free_kernel");
+    return SA_OK;
+}
+
+extern "C" int sa_paged_compact(int32_t *block_table, int32_t *refcount, int S, int max_pages, int64_t n_pages,
+                                int page, const sa_page_cache *caches, int n_caches, int64_t slot_bytes,
+                                int32_t *n_live, void *workspace, size_t workspace_bytes, void *stream) {
+    SA_TRACE("sa_paged_compact");
+    int vec = 16;
+    int rc = books_check("paged_compact", block_table, block_table ? (void *)block_table : (void *)n_live, refcount, S,
+                         max_pages, n_pages, page, 0);
+    if (rc == SA_OK) rc = caches_check("paged_compact", caches, n_caches, slot_bytes, vec);
+    if (rc) return rc;
+    if (!n_live || !aligned4(n_live)) return fail(SA_ERR_INVALID_ARG, "paged_compact: null or misaligned pointer");
+    BooksParams p{};
+    rc = books_params("paged_compact", p, block_table, nullptr, refcount, S, max_pages, n_pages, page, nullptr, nullptr,
+                      0, n_live, workspace, workspace_bytes);
+    if (rc) return rc;
+    cudaStream_t st = as_stream(stream);
+    launch_k("paged_compact_kernel", paged_compact_kernel, PB_CTAS, PB_THREADS, 0, st, p);
+    SA_CHECK_LAUNCH("paged_compact_kernel");
+    return copy_pages(p, caches, n_caches, slot_bytes, vec, true, st);
+}

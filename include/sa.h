@@ -361,6 +361,175 @@ int sa_topk_merge(const int32_t *cand_score, const int32_t *cand_idx, const int6
 int sa_index_shard(const int32_t *idx, int64_t n, int64_t key_lo, int64_t key_hi, int32_t *out, void *stream);
 
 /* --------------------------------------------------------------------------
+ * Sliding-window attention with sinks, forward and backward.  No page has a
+ * counterpart for the sinks: the window is the SpatialLM / NSA / HySparse2
+ * recent window as a layer of its own, with the first `sinks` keys of each
+ * sequence kept visible.  Query t of a sequence has position p = pos0 + t and
+ * sees
+ *   V(p) = { j <= min(p, n_k - 1) : p - j < window  or  j < sinks }
+ *   z_j = scale * q.k_j,  lse = log sum_{j in V} exp z_j,
+ *   out = sum_{j in V} exp(z_j - lse) v_j
+ * (an empty set gives out = 0, lse = -inf).  Backward, for dout:
+ *   P_j = exp(z_j - lse),  D = dout . out,  dS_j = P_j (dout . v_j - D)
+ *   dq = scale sum_j dS_j k_j,  dk_j = scale sum dS_j q,  dv_j = sum P_j dout
+ * (dk and dv summed over the queries that see j and the heads of its group).
+ *
+ * Two batch forms.  Dense (cu_q == cu_k == NULL): q [B, Tq, Hq, d], k and v
+ * [B, L, Hkv, d], pos0 = q_pos0 >= 0 for every sequence; keys behind the last
+ * query position are not read into any result.  Packed: q [Tq, Hq, d], k and
+ * v [L, Hkv, d] (Tq and L are the rows of the whole batch), sequence b has
+ * query rows cu_q[b] .. cu_q[b+1]-1 and key rows cu_k[b] .. cu_k[b+1]-1 (int32
+ * [B+1], device), and its last query stands at its last key: pos0 = n_k - n_q
+ * (queries before position 0 see nothing).  Any length may be 0.  Rows before
+ * cu[0] or from cu[B] on belong to no sequence: they reach no result, and
+ * their rows of out, lse, dq, dk and dv are left as they were.  max_q and
+ * max_k are upper bounds of the lengths (0 = not known).  A cu that decreases
+ * or leaves [0, rows], or a length above its bound, sets the device error
+ * word; what is cut off by that sequence's clamped ends is left as it was.
+ *
+ * dtype: bf16 or fp16 in the forward, bf16 in the backward (without a loss
+ * scale dS falls below fp16's normal range).  q, k, v and dout are strided:
+ * *_stride gives the elements between batches, tokens and heads (packed: the
+ * batch stride is not used); the last dimension is contiguous, every stride a
+ * multiple of 8 elements and every base 16-byte aligned.  out, dq [.., Hq, d],
+ * dk, dv [.., Hkv, d] have the inputs' type, lse is fp32 [.., Hq], natural log;
+ * all are written contiguous.  The backward reads the forward's out and lse
+ * through strides too (lse: any).  dq, dk and dv are written, not accumulated; the result does not
+ * depend on the order in which blocks run.  Values at keys outside V(p) do
+ * not reach a forward row, infinities and NaN included; the backward wants
+ * finite inputs within a sequence (what lies outside every sequence, or
+ * behind the last visible key, may hold anything).
+ * ------------------------------------------------------------------------ */
+enum sa_dtype { SA_BF16 = 0, SA_FP16 = 1 };
+
+typedef struct sa_sink_shape {
+    int32_t dtype;              /* sa_dtype */
+    int32_t B, Hq, Hkv, d;
+    int32_t window, sinks;      /* window >= 1 (counts the token itself), sinks >= 0 */
+    float scale;
+    int64_t Tq, L;              /* dense: per sequence; packed: rows of the batch */
+    int64_t q_pos0;             /* dense only */
+    int64_t max_q, max_k;       /* packed only: upper bounds of the lengths, 0 = not known */
+    int64_t q_stride[3], k_stride[3], v_stride[3];                  /* batch, token, head */
+    int64_t out_stride[3], dout_stride[3], lse_stride[3];           /* backward only */
+} sa_sink_shape;
+
+int sa_sink_attn_fwd(const sa_sink_shape *shape, const void *q, const void *k, const void *v, const int32_t *cu_q,
+                     const int32_t *cu_k, void *out, float *lse, void *stream);
+size_t sa_sink_attn_bwd_workspace_size(const sa_sink_shape *shape, int packed);
+int sa_sink_attn_bwd(const sa_sink_shape *shape, const void *q, const void *k, const void *v, const void *out,
+                     const float *lse, const void *dout, const int32_t *cu_q, const int32_t *cu_k, void *dq, void *dk,
+                     void *dv, void *workspace, size_t workspace_bytes, void *stream);
+
+/* --------------------------------------------------------------------------
+ * Attention of one new token over a paged key/value cache, split over the
+ * cache's length and joined by the log-sum-exp rule of sa_lse_combine.
+ * Sequence b holds n = seq_lens[b] tokens, the new one last (p = n - 1); its
+ * key j lies in slot j % page of page block_table[b, j / page] and is visible
+ * as in sa_sink_attn_fwd: window = 0 sees every key (sinks then says nothing),
+ * else p - j < window or j < sinks.  Table entries of pages without a visible
+ * key are not read (they may be -1: a trimmed middle), nor are slots without
+ * one, whatever they hold.  n = 0 gives out = 0, lse = -inf.
+ *   q [B, Hq, d]; caches [n_pages, page, Hkv, d] (bf16 or fp16); block_table
+ *   int32 [B, max_pages], seq_lens int32 [B] (device).  q, k_cache and v_cache
+ *   are strided (q: batch, head; caches: page, slot, head; multiples of 8
+ *   elements, last dimension contiguous).  out [B, Hq, d] and lse fp32 [B, Hq]
+ *   are contiguous.
+ * A visible key whose table entry lies outside [0, n_pages) is skipped, and a
+ * length outside [0, max_pages * page] is clamped; both set the device error
+ * word.  The split is chosen on the device from the lengths: no host copy,
+ * one launch shape for every step (a captured graph serves any lengths).
+ * workspace: sa_paged_attn_decode_workspace_size bytes, 16-byte aligned;
+ * calls that may overlap need one each.
+ * ------------------------------------------------------------------------ */
+typedef struct sa_paged_shape {
+    int32_t dtype;              /* sa_dtype */
+    int32_t B, Hq, Hkv, d;
+    int32_t page, max_pages;    /* tokens per page, entries per table row */
+    int32_t window, sinks;
+    float scale;
+    int64_t n_pages;
+    int64_t q_stride[2];                     /* batch, head */
+    int64_t k_stride[3], v_stride[3];        /* page, slot, head */
+} sa_paged_shape;
+
+size_t sa_paged_attn_decode_workspace_size(int B, int Hq, int Hkv, int d);
+int sa_paged_attn_decode(const sa_paged_shape *shape, const void *q, const void *k_cache, const void *v_cache,
+                         const int32_t *block_table, const int32_t *seq_lens, void *out, float *lse, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/* --------------------------------------------------------------------------
+ * The pages of a cache.  The books are device arrays of the caller:
+ *   block_table int32 [S, max_pages]  page of tokens i*page .. i*page+page-1
+ *                                     of a sequence, -1 = none
+ *   seq_lens    int32 [S]             tokens held
+ *   refcount    int32 [n_pages]       sequences that hold the page, 0 = free
+ * Every call is a few kernels on `stream`, reads its lists on the device and
+ * can be captured; calls on the same books must be ordered by the caller.
+ * Lists name sequences (rows of the table).  An entry that cannot be served
+ * changes nothing and is marked in the call's result; an entry that is wrong
+ * (outside the table, a sequence listed twice where that has no meaning, a
+ * page id outside the pool, a count that would fall below 0) also sets the
+ * device error word.
+ *
+ * sa_paged_extend: room for n_new[i] more tokens of sequence seqs[i].  The
+ *   pages that entry i lacks are the free pages of lowest id, after those of
+ *   the entries before it; refcount 1.  start[i] = the old length (the new
+ *   one is written to seq_lens), or -1 where the pool is used up (the pages
+ *   counted for it are not handed to later entries), where the row of the
+ *   table is too short, or where the entry is wrong.  seqs are distinct (a
+ *   repeated one is served at its first place).
+ * sa_paged_write: row r of k_new / v_new [N, Hkv, d], of list entry i (cu_new
+ *   int32 [n+1], cu_new[i] <= r < cu_new[i+1]; NULL: N = n, one row each) goes
+ *   to position start[i] + r - cu_new[i] of seqs[i]; entries with start < 0
+ *   and rows outside cu_new are skipped.  Elements of elem_bytes bytes, d *
+ *   elem_bytes and all strides (in elements; new: token, head; caches: page,
+ *   slot, head) multiples of 16 bytes.
+ * sa_paged_fork: sequence dst[i] (length 0 before) becomes a copy of src[i]:
+ *   full pages are shared (refcount + 1), a last page that is not full is
+ *   copied in each of the n_caches caches to a fresh page, taken as in
+ *   sa_paged_extend; -1 entries stay -1.  done[i] = 1, or 0 where no page was
+ *   left or the entry is wrong (src or dst outside the table, dst listed
+ *   twice (its first place counts), dst that is also a src, dst in use).
+ * sa_paged_free: window = 0: the pages of seqs[i] are given back (refcount -
+ *   1), its table row becomes -1, its length 0.  window > 0: only the pages
+ *   that no later query can see are given back, those whose positions are all
+ *   >= sinks and < seq_lens - window; their entries become -1, the length
+ *   stays (page must be given).  A sequence listed twice is freed once.
+ * sa_paged_compact: moves pages so that the live ones are 0 .. n_live-1: the
+ *   r-th live page with id >= n_live moves to the r-th free id below n_live,
+ *   in every cache, table and refcount following; n_live[0] is written.
+ *
+ * Caches are given as sa_page_cache: base pointer, bytes between pages and
+ * between slots, with slot_bytes bytes per slot (contiguous, the same for all)
+ * and `page` slots per page; pointers and byte counts are multiples of 4 (of 16
+ * for speed).
+ * workspace: sa_paged_books_workspace_size bytes (n = list length, 0 for
+ * compact), 16-byte aligned; sa_paged_write and sa_paged_free need none.
+ * ------------------------------------------------------------------------ */
+typedef struct sa_page_cache {
+    void *base;
+    int64_t page_stride, slot_stride;        /* bytes */
+} sa_page_cache;
+
+size_t sa_paged_books_workspace_size(int S, int n, int64_t n_pages);
+int sa_paged_extend(int32_t *block_table, int32_t *seq_lens, int32_t *refcount, int S, int max_pages, int64_t n_pages,
+                    int page, const int32_t *seqs, const int32_t *n_new, int n, int32_t *start, void *workspace,
+                    size_t workspace_bytes, void *stream);
+int sa_paged_write(const void *k_new, const void *v_new, void *k_cache, void *v_cache, const int32_t *block_table,
+                   const int32_t *seqs, const int32_t *start, const int32_t *cu_new, int n, int64_t N, int S,
+                   int max_pages, int64_t n_pages, int page, int Hkv, int d, int elem_bytes, const int64_t *k_new_stride,
+                   const int64_t *v_new_stride, const int64_t *k_stride, const int64_t *v_stride, void *stream);
+int sa_paged_fork(int32_t *block_table, int32_t *seq_lens, int32_t *refcount, int S, int max_pages, int64_t n_pages,
+                  int page, const int32_t *src, const int32_t *dst, int n, const sa_page_cache *caches, int n_caches,
+                  int64_t slot_bytes, int32_t *done, void *workspace, size_t workspace_bytes, void *stream);
+int sa_paged_free(int32_t *block_table, int32_t *seq_lens, int32_t *refcount, int S, int max_pages, int64_t n_pages,
+                  int page, const int32_t *seqs, int n, int window, int sinks, void *stream);
+int sa_paged_compact(int32_t *block_table, int32_t *refcount, int S, int max_pages, int64_t n_pages, int page,
+                     const sa_page_cache *caches, int n_caches, int64_t slot_bytes, int32_t *n_live, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/* --------------------------------------------------------------------------
  * Status helpers.
  * sa_check_device_status: waits for `stream`, reads and clears the device
  *   error word of the current device; returns SA_ERR_TIMEOUT if a kernel
