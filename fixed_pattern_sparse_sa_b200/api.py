@@ -578,8 +578,8 @@ def _need_rows(t, name: str, dtype, dev, shape):
         for i in range(len(st) - 1):
             if t.shape[i] > 1 and st[i] % n:
                 raise ValueError(f"{name}: strides must be multiples of 16 bytes, got {st}")
-            if t.shape[i] > 1 and st[i] < 0:
-                raise ValueError(f"{name}: negative stride")
+            if t.shape[i] > 1 and st[i] <= 0:
+                raise ValueError(f"{name}: a broadcast input is not supported, got strides {st}")
     return t
 
 

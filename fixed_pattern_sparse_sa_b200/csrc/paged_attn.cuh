@@ -96,16 +96,6 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const unsigned (&a)[4],
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
 }
-template <typename T>
-__device__ __forceinline__ unsigned pack2(float lo, float hi) {
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        return pack_bf16(lo, hi);
-    } else {
-        __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<unsigned *>(&h);
-    }
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const PagedParams p) {
     grid_dependency_sync();

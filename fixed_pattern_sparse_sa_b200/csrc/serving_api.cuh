@@ -7,6 +7,7 @@
 #include "paged_attn.cuh"
 #include "paged_books.cuh"
 #include "sink_attn.cuh"
+#include "sink_fwd_tc.cuh"
 
 // ---------------------------------------------------- sink-window attention --
 static bool strides_ok(const int64_t *s, int n, long long mul) {
@@ -38,6 +39,15 @@ static int sink_check(const char *what, const sa_sink_shape *s, const void *q, c
         return fail(SA_ERR_INVALID_ARG, "%s: null or misaligned pointer", what);
     if (!strides_ok(s->q_stride, 3, 8) || !strides_ok(s->k_stride, 3, 8) || !strides_ok(s->v_stride, 3, 8))
         return fail(SA_ERR_INVALID_ARG, "%s: strides must be multiples of 8 elements, not negative", what);
+    // rows that share memory (a broadcast input) are not taken: the copy engine's maps want a step
+    const int nb = cu_q ? 1 : s->B;
+    for (int i = 0; i < 3; ++i) {
+        const bool many_q = i == 0 ? nb > 1 : i == 1 ? s->Tq > 1 : s->Hq > 1;
+        const bool many_k = i == 0 ? nb > 1 : i == 1 ? s->L > 1 : s->Hkv > 1;
+        if ((many_q && s->q_stride[i] == 0) || (many_k && (s->k_stride[i] == 0 || s->v_stride[i] == 0)) ||
+            (bwd && many_q && s->dout_stride[i] == 0))
+            return fail(SA_ERR_INVALID_ARG, "%s: a stride of 0 (a broadcast input) is not supported", what);
+    }
     return SA_OK;
 }
 
@@ -59,12 +69,56 @@ static SinkParams sink_params(const sa_sink_shape *s, const void *q, const void 
 
 static unsigned sink_row_blocks(long long rows) { return (unsigned)std::min<long long>((rows + 3) / 4, 1 << 30); }
 
+// 4-D map over [batch, token, head, d] rows with the given strides (elements);
+// box = 64 columns (128 bytes) x box_heads x box_tokens, 128-byte swizzle.  A
+// dimension of size 1 is never stepped over, so its stride only has to be valid.
 template <typename T>
-static int sink_fwd_launch(const SinkParams &p, int d, cudaStream_t st) {
-    const unsigned g = sink_row_blocks((p.cu_q ? 1 : p.B) * p.Tq * p.Hq);
-    if (d == 64) launch_k("sink_fwd_rows_kernel<64>", sink_fwd_rows_kernel<T, 64>, g, 128, 0, st, p);
-    else launch_k("sink_fwd_rows_kernel<128>", sink_fwd_rows_kernel<T, 128>, g, 128, 0, st, p);
-    SA_CHECK_LAUNCH("sink_fwd_rows_kernel");
+static int rows_tensor_map(CUtensorMap *m, const void *base, int d, long long heads, long long tokens, long long batch,
+                           const long long *st, int box_heads, int box_tokens) {
+    TensorMapEncodeFn enc = tensor_map_encoder();
+    if (!enc) return fail(SA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens, (cuuint64_t)batch};
+    cuuint64_t strides[3] = {(cuuint64_t)(heads > 1 ? st[2] : d) * 2, (cuuint64_t)(tokens > 1 ? st[1] : d) * 2,
+                             (cuuint64_t)(batch > 1 ? st[0] : d) * 2};
+    cuuint32_t box[4] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_tokens, 1u};
+    cuuint32_t es[4] = {1u, 1u, 1u, 1u};
+    const CUresult r = enc(m, std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                           4, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(SA_ERR_INVALID_ARG, "a tensor of %lld x %lld x %lld rows with strides %lld, %lld, %lld cannot be "
+                    "described to the copy engine (%d)", batch, tokens, heads, st[0], st[1], st[2], (int)r);
+    return SA_OK;
+}
+
+static SinkTiles sink_tiles(const SinkParams &p) {
+    SinkTiles t{};
+    t.HB = std::min(p.G, 128);
+    t.HC = (p.G + 127) / 128;
+    t.TPT = 128 / t.HB;
+    const long long TI = 2 * t.TPT;
+    t.blocks = p.cu_q ? p.Tq / TI + p.B : p.B * ((p.Tq + TI - 1) / TI);
+    t.items = t.blocks * p.Hkv * t.HC;
+    return t;
+}
+
+template <typename T, int D>
+static int sink_fwd_launch(const SinkParams &p, cudaStream_t st) {
+    const SinkTiles t = sink_tiles(p);
+    const long long nb = p.cu_q ? 1 : p.B;
+    CUtensorMap qm, km, vm;
+    // without keys nothing is loaded; the maps only have to be valid
+    const void *k = p.L ? p.k : p.q, *v = p.L ? p.v : p.q;
+    int rc = rows_tensor_map<T>(&qm, p.q, D, p.Hq, p.Tq, nb, p.q_s, t.HB, t.TPT);
+    if (!rc) rc = rows_tensor_map<T>(&km, k, D, p.Hkv, std::max(p.L, 1ll), nb, p.k_s, 1, SF_KT);
+    if (!rc) rc = rows_tensor_map<T>(&vm, v, D, p.Hkv, std::max(p.L, 1ll), nb, p.v_s, 1, SF_KT);
+    if (!rc) rc = set_smem(sink_fwd_tc_kernel<T, D>, SfSmem<D>::ALLOC);
+    if (rc) return rc;
+    const unsigned grid = (unsigned)std::min<long long>(t.items, sm_count());
+    launch_k("sink_fwd_tc_kernel", sink_fwd_tc_kernel<T, D>, grid, SF_THREADS, SfSmem<D>::ALLOC, st, qm, km, vm, p, t);
+    SA_CHECK_LAUNCH("sink_fwd_tc_kernel");
     return SA_OK;
 }
 
@@ -81,8 +135,9 @@ extern "C" int sa_sink_attn_fwd(const sa_sink_shape *shape, const void *q, const
     if (rc) return rc;
     p.out = out; p.lse = lse;
     cudaStream_t st = as_stream(stream);
-    return shape->dtype == SA_BF16 ? sink_fwd_launch<__nv_bfloat16>(p, shape->d, st)
-                                   : sink_fwd_launch<__half>(p, shape->d, st);
+    if (shape->dtype == SA_BF16)
+        return shape->d == 64 ? sink_fwd_launch<__nv_bfloat16, 64>(p, st) : sink_fwd_launch<__nv_bfloat16, 128>(p, st);
+    return shape->d == 64 ? sink_fwd_launch<__half, 64>(p, st) : sink_fwd_launch<__half, 128>(p, st);
 }
 
 extern "C" size_t sa_sink_attn_bwd_workspace_size(const sa_sink_shape *s, int packed) {

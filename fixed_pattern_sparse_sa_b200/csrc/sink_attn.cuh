@@ -90,45 +90,14 @@ template <typename T> __device__ __forceinline__ T from_f(float x);
 template <> __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16(x); }
 template <> __device__ __forceinline__ __half from_f(float x) { return __float2half(x); }
 
-// One warp per query row and head; a lane holds D / 32 elements and every key
-// costs one dot product over the warp.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) sink_fwd_rows_kernel(const SinkParams p) {
-    grid_dependency_sync();
-    sink_report(p);
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long rows = (p.cu_q ? 1 : p.B) * p.Tq * p.Hq;
-    for (long long w = blockIdx.x * 4ll + (threadIdx.x >> 5); w < rows; w += gridDim.x * 4ll) {
-        const int h = (int)(w % p.Hq), g = h / p.G;
-        const long long r = w / p.Hq;
-        const int b = p.cu_q ? sink_find(p.cu_q, p.B, r) : (int)(r / p.Tq);
-        if (b < 0) continue;
-        const SinkSeq s = sink_seq(p, b);
-        const long long t = p.cu_q ? r - s.q0 : r % p.Tq;
-        if (t < 0 || t >= s.nq) continue;
-        const long long bq = p.cu_q ? 0 : b;
-        const T *q = (const T *)p.q + bq * p.q_s[0] + (s.q0 + t) * p.q_s[1] + h * p.q_s[2] + lane * E;
-        const T *kb = (const T *)p.k + bq * p.k_s[0] + s.k0 * p.k_s[1] + g * p.k_s[2] + lane * E;
-        const T *vb = (const T *)p.v + bq * p.v_s[0] + s.k0 * p.v_s[1] + g * p.v_s[2] + lane * E;
-        float qf[E], o[E] = {}, m = -INFINITY, l = 0.f;
-        for (int e = 0; e < E; ++e) qf[e] = to_f(q[e]);
-        int s1, lo, hi;
-        sink_visible(p, s.nk, s.pos0 + t, s1, lo, hi);
-        for (int j = s1 > 0 ? 0 : lo; j < hi; j = j + 1 == s1 ? lo : j + 1) {
-            float z = 0.f;
-            for (int e = 0; e < E; ++e) z += qf[e] * to_f(kb[j * p.k_s[1] + e]);
-            z = warp_sum(z) * p.scale_log2;
-            const float mn = fmaxf(m, z), a = m == -INFINITY ? 0.f : exp2f(m - mn);
-            const float w_ = mn == -INFINITY ? 0.f : exp2f(z - mn);
-            l = l * a + w_;
-            for (int e = 0; e < E; ++e) o[e] = o[e] * a + w_ * to_f(vb[j * p.v_s[1] + e]);
-            m = mn;
-        }
-        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-        T *out = (T *)p.out + w * D + lane * E;
-        for (int e = 0; e < E; ++e) out[e] = from_f<T>(o[e] * inv);
-        if (lane == 0) p.lse[w] = l > 0.f ? (m + log2f(l)) * kLn2 : l == 0.f ? -INFINITY : l;
+// two values as a packed pair, the first in the low half
+template <typename T>
+__device__ __forceinline__ unsigned pack2(float lo, float hi) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        return pack_bf16(lo, hi);
+    } else {
+        __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<unsigned *>(&h);
     }
 }
 

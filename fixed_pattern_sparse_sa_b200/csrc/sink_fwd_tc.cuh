@@ -1,0 +1,558 @@
+// sink_fwd_tc.cuh -- forward of the sink-window attention on the tcgen05
+// tensor cores.
+//
+// A work item is two row tiles (A, B) of 128 rows: TPT consecutive queries x
+// the HB heads of a KV group (HB = min(G, 128), TPT = 128 / HB), row =
+// query * HB + head, so both tiles read the same keys.  What any of the rows
+// sees is two contiguous key ranges, [0, s_end) of the sinks and [band_lo,
+// band_hi) of the windows, walked in tiles of up to 128 keys.  Per tile and
+// row tile
+//   S = Q K^T (tcgen05.mma, fp32 in tensor memory),  P = 2^(S c - m),  O += P V
+// with the running maximum m and sum of a row held by one thread; P replaces
+// S in tensor memory and is the A operand of the second product.  m is raised
+// (and O rescaled) only when a tile exceeds it by more than 2^8.  P is
+// rounded to the inputs' type (half a step a weight, as the output is).
+//
+// The tensor cores and the softmax alternate between A and B: while one
+// tile's scores are turned into weights the other's products run.  Queue
+// order: P.V of A(j), S of A(j+1), P.V of B(j), S of B(j+1), across items.
+// A tile of n < 128 keys costs N = n (rounded up to 16) columns in the first
+// product and n rows in the second, so short sinks and window ends are cheap;
+// a row tile skips key tiles that none of its rows sees.
+//
+// Rows of V that not every row of the item sees are cleaned in shared memory
+// first: 0 * inf would put NaN into rows that must not see them.  What is not
+// finite there is added back, at the end, to the rows that do see it.
+//
+// Warps: 0-3 softmax and epilogue of A (thread = row), 4-7 of B, 8 TMA
+// producer, 9 MMA issuer and TMEM owner.  Every wait is bounded; a timeout
+// sets ERR_TIMEOUT and the CTA drains and exits.
+#pragma once
+
+#include "attn_tc.cuh"
+#include "sink_attn.cuh"
+
+namespace sa {
+
+constexpr int SF_KT = 128;               // keys per tile
+constexpr int SF_SLOTS = 5;              // ring of K and V tiles
+constexpr int SF_THREADS = 320;
+constexpr uint32_t SF_TM_S = 0;          // S / P of A, B: 128 columns each
+constexpr uint32_t SF_TM_O = 256;        // O of A, B: 128 columns each
+constexpr uint32_t SF_TM_COLS = 512;
+constexpr float SF_RAISE = 8.f;
+
+template <int D>
+struct SfSmem {
+    static constexpr int TILE = 128 * D * 2;               // Q, K or V tile: D / 64 halves of 128 rows x 128 B
+    static constexpr int OFF_Q = 0;                        // A, B
+    static constexpr int OFF_KV = OFF_Q + 2 * TILE;
+    static constexpr int OFF_BAR = OFF_KV + SF_SLOTS * TILE;
+    // q_full[2], q_empty[2], kv_full[S], kv_empty[S], s_full[2], p_full[2], pv_done[2], o_full[2], drain
+    static constexpr int N_BAR = 4 + 2 * SF_SLOTS + 8 + 1;
+    static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;   // tmem slot, abort flag, dirty flag
+    static constexpr int TOTAL = OFF_MISC + 32;
+    static constexpr int ALLOC = TOTAL + 1024;
+};
+
+struct SinkTiles {
+    int HB, HC, TPT;         // heads per row tile, head chunks per group, queries per row tile
+    long long blocks;        // query blocks of 2 * TPT over the batch (packed: an upper bound)
+    long long items;         // blocks * Hkv * HC
+};
+
+// One work item: its sequence, rows and key tiles.
+struct SinkItem {
+    SinkSeq s;
+    int b, hk, h0, nh;       // h0: first head, nh: heads of the tile that belong to the group
+    int t0, nq_i[2];         // first query; queries of A and B
+    int band_lo, band_hi, s_end, n_sink, nt;
+    int lo_min[2], hi_max[2], s1_max[2];     // over the rows of A and B
+    int clean_lo, clean_hi;  // keys of [band_lo, clean_lo) and [clean_hi, band_hi) are not seen by every row
+
+    __device__ __forceinline__ void tile(int j, int &k0, int &n) const {
+        if (j < n_sink) {
+            k0 = j * SF_KT;
+            n = min(SF_KT, s_end - k0);
+        } else {
+            k0 = band_lo + (j - n_sink) * SF_KT;
+            n = min(SF_KT, band_hi - k0);
+        }
+    }
+    // does any row of row tile i see a key of tile j?
+    __device__ __forceinline__ bool active(int i, int j) const {
+        if ((i ? nq_i[1] : nq_i[0]) == 0) return false;
+        if (j < n_sink) return true;
+        int k0, n;
+        tile(j, k0, n);
+        return k0 < (i ? hi_max[1] : hi_max[0]) &&
+               (k0 + n > (i ? lo_min[1] : lo_min[0]) || k0 < (i ? s1_max[1] : s1_max[0]));
+    }
+};
+__device__ __forceinline__ bool sink_item(const SinkParams &p, const SinkTiles &tl, long long it, SinkItem &x) {
+    const int hh = (int)(it % (p.Hkv * tl.HC));
+    const long long blk = it / (p.Hkv * tl.HC);
+    x.hk = hh / tl.HC;
+    const int hc = hh % tl.HC, TI = 2 * tl.TPT;
+    x.h0 = x.hk * p.G + hc * tl.HB;
+    x.nh = min(tl.HB, p.G - hc * tl.HB);
+    long long local;
+    if (!p.cu_q) {
+        const long long per = (p.Tq + TI - 1) / TI;
+        x.b = (int)(blk / per);
+        local = blk % per;
+    } else {
+        // sequence b starts at block cu[b] / TI + b: the last start at or before blk
+        int lo = 0, hi = p.B;
+        while (hi - lo > 1) {
+            const int m = (lo + hi) / 2;
+            const long long c = min(max((long long)__ldg(p.cu_q + m), 0ll), p.Tq);
+            if (c / TI + m <= blk) lo = m; else hi = m;
+        }
+        x.b = lo;
+        local = blk - (min(max((long long)__ldg(p.cu_q + lo), 0ll), p.Tq) / TI + lo);
+    }
+    x.s = sink_seq(p, x.b);
+    if (local < 0 || local * TI >= x.s.nq) return false;
+    x.t0 = (int)(local * TI);
+    int s1, lo, hi;
+    sink_visible(p, x.s.nk, x.s.pos0 + x.t0, s1, lo, hi);
+    x.band_lo = lo;
+    x.clean_hi = hi;
+    x.s_end = min(p.sinks, lo);
+    x.clean_lo = lo;
+    x.band_hi = hi;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int ta = x.t0 + i * tl.TPT;
+        x.nq_i[i] = min(tl.TPT, x.s.nq - ta);
+        if (x.nq_i[i] <= 0) {
+            x.nq_i[i] = 0;
+            x.lo_min[i] = x.hi_max[i] = x.s1_max[i] = 0;
+            continue;
+        }
+        sink_visible(p, x.s.nk, x.s.pos0 + ta, s1, lo, hi);
+        x.lo_min[i] = lo;
+        sink_visible(p, x.s.nk, x.s.pos0 + ta + x.nq_i[i] - 1, s1, lo, hi);
+        x.hi_max[i] = hi;
+        x.s1_max[i] = s1;
+        x.band_hi = hi;
+        x.clean_lo = lo;
+    }
+    x.n_sink = (x.s_end + SF_KT - 1) / SF_KT;
+    x.nt = x.n_sink + (x.band_hi - x.band_lo + SF_KT - 1) / SF_KT;
+    return true;
+}
+
+// 32 lanes x 32 consecutive 32-bit columns
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// box of a 4-D tensor map at (x, y, z, w)
+__device__ __forceinline__ void load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(tc::smem_u32(bar))
+        : "memory");
+}
+// kind::f16 instruction descriptor operand format of T
+template <typename T>
+__host__ __device__ constexpr uint32_t ab_format() { return std::is_same<T, __nv_bfloat16>::value ? 1u : 0u; }
+// Does a pair of 16-bit values hold an infinity or NaN (exponent all ones)?
+template <typename T>
+__device__ __forceinline__ bool not_finite16(uint32_t x) {
+    constexpr uint32_t E = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+    return (x & E) == E;
+}
+// bits [lo, hi) of a 32-bit word, bounds clamped
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+    const uint32_t a = lo <= 0 ? 0xffffffffu : lo >= 32 ? 0u : 0xffffffffu << lo;
+    const uint32_t b = hi <= 0 ? 0u : hi >= 32 ? 0xffffffffu : ~(0xffffffffu << hi);
+    return a & b;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(SF_THREADS, 1)
+    sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap, const __grid_constant__ SinkParams p,
+                       const __grid_constant__ SinkTiles tl) {
+    grid_dependency_sync();
+    using L = SfSmem<D>;
+    constexpr int HALVES = D / 64;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
+    uint64_t *q_full = bars, *q_empty = bars + 2, *kv_full = bars + 4, *kv_empty = kv_full + SF_SLOTS;
+    uint64_t *s_full = kv_empty + SF_SLOTS, *p_full = s_full + 2, *pv_done = p_full + 2, *o_full = pv_done + 2;
+    uint64_t *drain = o_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
+    volatile int *dirty = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 8);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (warp == 9) {
+        tc::tmem_alloc(tmem_slot, SF_TM_COLS);
+        tc::tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(q_full + i, 1); tc::mbar_init(q_empty + i, 1);
+            tc::mbar_init(s_full + i, 1); tc::mbar_init(p_full + i, 128); tc::mbar_init(pv_done + i, 1);
+            tc::mbar_init(o_full + i, 1);
+        }
+        for (int i = 0; i < SF_SLOTS; ++i) { tc::mbar_init(kv_full + i, 1); tc::mbar_init(kv_empty + i, 1); }
+        tc::mbar_init(drain, 1);
+        *abort_flag = 0;
+        *dirty = 0;
+        tc::mbar_fence_init();
+    }
+    sink_report(p);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    auto fail = [&]() {
+        raise_error(p.err, ERR_TIMEOUT);
+        *abort_flag = 1;
+    };
+
+    if (warp == 8) {
+        // ------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            bool ok = true;
+            int qn = 0, kv = 0;                       // items and ring tiles loaded
+            for (long long it = blockIdx.x; it < tl.items && ok; it += gridDim.x) {
+                SinkItem x;
+                if (!sink_item(p, tl, it, x) || x.nt == 0) continue;
+                const int qb = p.cu_q ? 0 : x.b;
+                auto load_q = [&](int i) -> bool {
+                    if (!atc::wait(q_empty + i, (qn & 1) ^ 1, abort_flag)) return false;
+                    atc::expect_tx(q_full + i, HALVES * 128 * tl.HB * tl.TPT);
+                    for (int h = 0; h < HALVES; ++h)
+                        load_4d(smem + L::OFF_Q + i * L::TILE + h * (128 * 128), &qmap, h * 64, x.h0,
+                                (int)(x.s.q0 + x.t0 + i * tl.TPT), qb, q_full + i);
+                    return true;
+                };
+                auto load_kv = [&](const CUtensorMap *map, int j) -> bool {
+                    const int sl = kv % SF_SLOTS;
+                    if (!atc::wait(kv_empty + sl, ((kv / SF_SLOTS) & 1) ^ 1, abort_flag)) return false;
+                    int k0, n;
+                    x.tile(j, k0, n);
+                    atc::expect_tx(kv_full + sl, L::TILE);
+                    for (int h = 0; h < HALVES; ++h)
+                        load_4d(smem + L::OFF_KV + sl * L::TILE + h * (SF_KT * 128), map, h * 64, x.hk,
+                                (int)(x.s.k0 + k0), qb, kv_full + sl);
+                    ++kv;
+                    return true;
+                };
+                ok = load_q(0) && load_kv(&kmap, 0) && load_q(1);
+                if (!ok) break;
+                ++qn;
+                ok = load_kv(&vmap, 0);
+                for (int j = 1; j < x.nt && ok; ++j) ok = load_kv(&kmap, j) && load_kv(&vmap, j);
+            }
+            if (!ok) fail();
+            // let the copies land before the CTA exits
+            for (int i = 0; i < 2 && qn > 0; ++i) tc::mbar_wait_bounded(q_full + i, (qn - 1) & 1, ATC_WAIT);
+            for (int i = 0; i < SF_SLOTS && i < kv; ++i) {
+                const int t = kv - 1 - i;
+                tc::mbar_wait_bounded(kv_full + t % SF_SLOTS, (t / SF_SLOTS) & 1, ATC_WAIT);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // --------------------------------------------------------------- MMA
+        if (lane == 0) {
+            constexpr uint32_t F = ab_format<T>();
+            constexpr uint32_t ID_O = tc::make_idesc(1, F, 128, D) | (1u << 16);    // B (V) MN-major
+            bool ok = true;
+            int qn = 0, kv = 0;                       // items begun (Q), ring tiles
+            int pn[2] = {0, 0};
+            struct Cur { SinkItem x; int j; bool valid; };
+            Cur cur, nxt;
+            long long it = blockIdx.x;
+            auto fetch = [&](Cur &c) {                // the next item that has keys
+                c.valid = false;
+                c.j = 0;
+                for (; it < tl.items; it += gridDim.x)
+                    if (sink_item(p, tl, it, c.x) && c.x.nt > 0) {
+                        c.valid = true;
+                        it += gridDim.x;
+                        return;
+                    }
+            };
+            // S of row tile i for tile j of item x; ring tile ks holds its keys
+            auto issue_s = [&](const SinkItem &x, int i, int j, int ks) -> bool {
+                if (j == 0 && !atc::wait(q_full + i, (qn - 1) & 1, abort_flag)) return false;
+                if (!atc::wait(kv_full + ks % SF_SLOTS, (ks / SF_SLOTS) & 1, abort_flag)) return false;
+                if (x.active(i, j)) {
+                    int k0, n;
+                    x.tile(j, k0, n);
+                    const uint32_t id = tc::make_idesc(1, F, 128, (n + 15) & ~15);
+                    tc::fence_after_sync();
+                    const uint32_t qa = tc::smem_u32(smem + L::OFF_Q + i * L::TILE);
+                    const uint32_t ka = tc::smem_u32(smem + L::OFF_KV + (ks % SF_SLOTS) * L::TILE);
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        const int h = c / 4, kk = c % 4;
+                        tc::mma_bf16(tmem + SF_TM_S + i * 128, atc::desc_sw128(qa + h * (128 * 128) + kk * 32, 16, 1024),
+                                     atc::desc_sw128(ka + h * (SF_KT * 128) + kk * 32, 16, 1024), id, c > 0 ? 1u : 0u);
+                    }
+                    tc::mma_commit(s_full + i);
+                }
+                if (j == x.nt - 1) tc::mma_commit(q_empty + i);
+                return true;
+            };
+            bool begun[2] = {false, false};           // O of the current item holds a product
+            auto issue_pv = [&](const SinkItem &x, int i, int j, int vs) -> bool {
+                if (!atc::wait(kv_full + vs % SF_SLOTS, (vs / SF_SLOTS) & 1, abort_flag)) return false;
+                if (!x.active(i, j)) return true;
+                // the softmax warps write an item's first P after they have read the O of the item before
+                if (!atc::wait(p_full + i, pn[i] & 1, abort_flag)) return false;
+                ++pn[i];
+                tc::fence_after_sync();
+                int k0, n;
+                x.tile(j, k0, n);
+                const uint32_t va = tc::smem_u32(smem + L::OFF_KV + (vs % SF_SLOTS) * L::TILE);
+                const int steps = (n + 15) / 16;
+                for (int c = 0; c < steps; ++c)
+                    // V: MN-major, 64-column atoms SF_KT * 128 B apart, 8-key groups 1 KB apart
+                    tc::mma_bf16_ts(tmem + SF_TM_O + i * 128, tmem + SF_TM_S + i * 128 + c * 8,
+                                    atc::desc_sw128(va + c * 2048, SF_KT * 128, 1024), ID_O,
+                                    begun[i] || c > 0 ? 1u : 0u);
+                begun[i] = true;
+                tc::mma_commit(pv_done + i);
+                return true;
+            };
+            fetch(cur);
+            if (cur.valid) {
+                ++qn;
+                ok = issue_s(cur.x, 0, 0, 0) && issue_s(cur.x, 1, 0, 0);
+                if (ok) tc::mma_commit(kv_empty + 0);
+            }
+            // ring tiles: kv = K of the current tile, kv + 1 = V, kv + 2 = K of the next
+            while (ok && cur.valid) {
+                const bool last = cur.j + 1 == cur.x.nt;
+                if (last) {
+                    fetch(nxt);
+                    if (nxt.valid) ++qn;
+                }
+                const bool more = !last || nxt.valid;
+                const SinkItem &nx = last ? nxt.x : cur.x;
+                const int nj = last ? 0 : cur.j + 1;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (!ok) break;
+                    ok = issue_pv(cur.x, i, cur.j, kv + 1);
+                    if (ok && last && begun[i]) tc::mma_commit(o_full + i);
+                    if (ok && i == 1) tc::mma_commit(kv_empty + (kv + 1) % SF_SLOTS);
+                    if (ok && more) ok = issue_s(nx, i, nj, kv + 2);
+                }
+                if (!ok) break;
+                if (more) tc::mma_commit(kv_empty + (kv + 2) % SF_SLOTS);
+                kv += 2;
+                if (last) {
+                    begun[0] = begun[1] = false;
+                    cur = nxt;
+                } else {
+                    ++cur.j;
+                }
+            }
+            if (!ok) fail();
+            tc::mma_commit(drain);
+            tc::mbar_wait_bounded(drain, 0, ATC_WAIT);
+        }
+        __syncwarp();
+    } else {
+        // --------------------------------------------- softmax and epilogue
+        const int i = warp >> 2, r = (warp & 3) * 32 + lane;      // row tile, row of it
+        const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lrow + SF_TM_S + i * 128, tO = tmem + lrow + SF_TM_O + i * 128;
+        const int tt = r / tl.HB, hh = r - tt * tl.HB;
+        auto agree = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
+        bool ok = true;
+        int sn = 0, on = 0, kv = 0;                   // S tiles, items with an O, ring tiles before this item
+        for (long long it = blockIdx.x; it < tl.items && ok; it += gridDim.x) {
+            SinkItem x;
+            if (!sink_item(p, tl, it, x)) continue;
+            const int t = x.t0 + i * tl.TPT + tt;
+            const bool row_ok = tt < x.nq_i[i] && hh < x.nh;
+            int s1 = 0, lo = -(1 << 30), hi = 1 << 30;    // rows of nobody: anything, never written
+            if (row_ok) sink_visible(p, x.s.nk, x.s.pos0 + t, s1, lo, hi);
+            float m = -INFINITY, l = 0.f;
+            bool first = true;
+            for (int j = 0; j < x.nt; ++j) {
+                if (!x.active(i, j)) continue;
+                int k0, n;
+                x.tile(j, k0, n);
+                // the first row tile that uses this V tile cleans the rows that not every row sees
+                const bool sink = j < x.n_sink;
+                const int ca = sink ? 0 : min(n, max(0, x.clean_lo - k0)), cb = sink ? n : min(n, max(0, x.clean_hi - k0));
+                const int n16 = (n + 15) & ~15;
+                const bool dirt = ca > 0 || cb < n16;
+                if (dirt && (i == 0 || !x.active(0, j))) {
+                    const int vs = kv + 2 * j + 1, sl = vs % SF_SLOTS;
+                    if (!agree(atc::wait(kv_full + sl, (vs / SF_SLOTS) & 1, abort_flag))) { ok = false; break; }
+                    // 16-byte units of the rows [0, ca) and [cb, n16)
+                    constexpr int U = D / 8;
+                    const int rows = ca + (n16 - max(cb, ca));
+                    bool found = false;
+                    for (int u = r; u < rows * U; u += 128) {
+                        int key = u / U;
+                        const int c = u % U;
+                        if (key >= ca) key += max(cb, ca) - ca;
+                        uint4 *at = reinterpret_cast<uint4 *>(smem + L::OFF_KV + sl * L::TILE + (c / 8) * (SF_KT * 128) +
+                                                              key * 128 + (((c & 7) ^ (key & 7)) * 16));
+                        if (key >= n) {
+                            *at = make_uint4(0u, 0u, 0u, 0u);
+                            continue;
+                        }
+                        uint4 v = *at;
+                        uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+                        bool bad = false;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (not_finite16<T>(w[e])) { w[e] &= 0xffff0000u; bad = true; }
+                            if (not_finite16<T>(w[e] >> 16)) { w[e] &= 0xffffu; bad = true; }
+                        }
+                        if (bad) {
+                            *at = v;
+                            found = true;
+                        }
+                    }
+                    if (found) *dirty = 1;
+                    tc::fence_proxy_async_smem();
+                }
+                if (!agree(atc::wait(s_full + i, sn & 1, abort_flag))) { ok = false; break; }
+                tc::fence_after_sync();
+                uint32_t s[SF_KT];
+#pragma unroll
+                for (int c = 0; c < SF_KT; c += 32)
+                    if (c < n) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(s + c));
+                tc::tmem_ld_wait();
+                const bool whole = n == SF_KT && ((k0 >= lo && k0 + n <= hi) || k0 + n <= s1);
+                if (!__all_sync(0xffffffffu, whole)) {
+#pragma unroll
+                    for (int c = 0; c < SF_KT; c += 32) {
+                        const uint32_t vis = c < n ? (bit_range(lo - k0 - c, hi - k0 - c) | bit_range(0, s1 - k0 - c)) &
+                                                         bit_range(0, n - c)
+                                                   : 0u;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((vis >> e) & 1u)) s[c + e] = __float_as_uint(-INFINITY);
+                    }
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < SF_KT; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                const bool raise = mt > m + (m == -INFINITY ? 0.f : SF_RAISE);
+                float alpha = 1.f;
+                if (raise) {
+                    alpha = m == -INFINITY ? 0.f : ex2_fast(m - mt);
+                    m = mt;
+                    l *= alpha;
+                }
+                if (!first && __any_sync(0xffffffffu, raise)) {
+                    if (!agree(atc::wait(pv_done + i, (sn - 1) & 1, abort_flag))) { ok = false; break; }
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o16[16];
+                        tc::tmem_ld16(tO + c, o16);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o16[e] = __float_as_uint(__uint_as_float(o16[e]) * alpha);
+                        atc::tmem_st16(tO + c, o16);
+                    }
+                }
+                first = false;
+                ++sn;
+                const float nb = m == -INFINITY ? 0.f : -m;
+                float rs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < SF_KT; c += 32) {
+                    if (c < n) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float p0 = ex2_fast(fmaf(__uint_as_float(s[c + e]), p.scale_log2, nb));
+                            const float p1 = ex2_fast(fmaf(__uint_as_float(s[c + e + 1]), p.scale_log2, nb));
+                            rs[e & 2] += p0;
+                            rs[(e & 2) + 1] += p1;
+                            pk[e / 2] = pack2<T>(p0, p1);
+                        }
+                        atc::tmem_st16(tS + c / 2, pk);
+                    }
+                }
+                l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+                atc::tmem_st_wait();
+                tc::fence_before_sync();
+                atc::arrive(p_full + i);
+            }
+            if (!ok) break;
+            // ------------------------------------------------------ epilogue
+            const long long orow = ((p.cu_q ? 0 : (long long)x.b * p.Tq) + x.s.q0 + t) * p.Hq + x.h0 + hh;
+            if (!first) {
+                if (!agree(atc::wait(o_full + i, on & 1, abort_flag))) { ok = false; break; }
+                tc::fence_after_sync();
+                ++on;
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const bool patch = *dirty != 0;            // set once, for every later item of this CTA
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+                uint32_t o16[16];
+                if (first) {                          // no key tile: O holds nothing of this item
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o16[e] = 0u;
+                } else {
+                    tc::tmem_ld16(tO + c, o16);
+                    tc::tmem_ld_wait();
+                }
+                if (row_ok) {
+                    float f[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) f[e] = l == 0.f ? 0.f : __uint_as_float(o16[e]) * inv;
+                    if (patch) {
+                        const T *vb = (const T *)p.v + (p.cu_q ? 0 : x.b) * p.v_s[0] + x.s.k0 * p.v_s[1] +
+                                      x.hk * p.v_s[2] + c;
+                        for (int k = x.band_lo; k < x.band_hi; ++k) {
+                            if (k == x.clean_lo && k < x.clean_hi) k = x.clean_hi;
+                            if (k >= x.band_hi) break;
+                            if (!(k < s1 || (k >= lo && k < hi))) continue;
+                            for (int e = 0; e < 16; ++e) {
+                                const float v = to_f(vb[k * p.v_s[1] + e]);
+                                if (!isfinite(v)) f[e] += v;
+                            }
+                        }
+                    }
+                    uint32_t w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = pack2<T>(f[2 * e], f[2 * e + 1]);
+                    uint4 *dst = reinterpret_cast<uint4 *>((T *)p.out + orow * D + c);
+                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            }
+            if (row_ok) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            tc::fence_before_sync();
+            kv += 2 * x.nt;
+        }
+        if (!ok) fail();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 9) tc::tmem_dealloc(tmem, SF_TM_COLS);
+}
+
+}  // namespace sa

@@ -391,7 +391,8 @@ int sa_index_shard(const int32_t *idx, int64_t n, int64_t key_lo, int64_t key_hi
  * scale dS falls below fp16's normal range).  q, k, v and dout are strided:
  * *_stride gives the elements between batches, tokens and heads (packed: the
  * batch stride is not used); the last dimension is contiguous, every stride a
- * multiple of 8 elements and every base 16-byte aligned.  out, dq [.., Hq, d],
+ * multiple of 8 elements and not 0 over more than one step (no broadcast
+ * inputs), every base 16-byte aligned.  out, dq [.., Hq, d],
  * dk, dv [.., Hkv, d] have the inputs' type, lse is fp32 [.., Hq], natural log;
  * all are written contiguous.  The backward reads the forward's out and lse
  * through strides too (lse: any).  dq, dk and dv are written, not accumulated; the result does not
