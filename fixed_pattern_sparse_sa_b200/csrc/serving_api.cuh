@@ -23,7 +23,7 @@ static int sink_check(const char *what, const sa_sink_shape *s, const void *q, c
         s->max_q < 0 || s->max_k < 0)
         return fail(SA_ERR_INVALID_ARG, "%s: bad sizes (Hq a multiple of Hkv)", what);
     if (s->window < 1 || s->sinks < 0) return fail(SA_ERR_INVALID_ARG, "%s: window >= 1, sinks >= 0", what);
-    if (!std::isfinite(s->scale)) return fail(SA_ERR_INVALID_ARG, "%s: scale", what);
+    if (!std::isfinite(s->scale) || s->scale <= 0.f) return fail(SA_ERR_INVALID_ARG, "%s: scale must be positive", what);
     if (s->d != 64 && s->d != 128) return fail(SA_ERR_UNSUPPORTED, "%s: head dim %d (64 or 128)", what, s->d);
     if (s->dtype != SA_BF16 && (bwd || s->dtype != SA_FP16))
         return fail(SA_ERR_UNSUPPORTED, "%s: dtype %d", what, s->dtype);
@@ -225,7 +225,8 @@ extern "C" int sa_paged_attn_decode(const sa_paged_shape *s, const void *q, cons
     if (s->B < 0 || s->Hq <= 0 || s->Hkv <= 0 || s->Hq % s->Hkv || s->page <= 0 || s->max_pages < 0 || s->n_pages < 0 ||
         s->window < 0 || s->sinks < 0)
         return fail(SA_ERR_INVALID_ARG, "paged_attn_decode: bad sizes (Hq a multiple of Hkv)");
-    if (!std::isfinite(s->scale)) return fail(SA_ERR_INVALID_ARG, "paged_attn_decode: scale");
+    if (!std::isfinite(s->scale) || s->scale <= 0.f)
+        return fail(SA_ERR_INVALID_ARG, "paged_attn_decode: scale must be positive");
     if (s->d != 64 && s->d != 128) return fail(SA_ERR_UNSUPPORTED, "paged_attn_decode: head dim %d (64 or 128)", s->d);
     if (s->dtype != SA_BF16 && s->dtype != SA_FP16)
         return fail(SA_ERR_UNSUPPORTED, "paged_attn_decode: dtype %d", s->dtype);

@@ -36,7 +36,9 @@ namespace sa {
 
 constexpr int SF_KT = 128;               // keys per tile
 constexpr int SF_SLOTS = 5;              // ring of K and V tiles
-constexpr int SF_THREADS = 320;
+constexpr int SF_THREADS = 384;          // 3 warpgroups; warps 10 and 11 only give their registers away
+// registers a thread: launched with 168 (384 x 168 = 64512); 2 x 208 + 88 = 3 x 168
+constexpr int SF_REGS_SOFTMAX = 208, SF_REGS_ISSUE = 88;
 constexpr uint32_t SF_TM_S = 0;          // S / P of A, B: 128 columns each
 constexpr uint32_t SF_TM_O = 256;        // O of A, B: 128 columns each
 constexpr uint32_t SF_TM_COLS = 512;
@@ -173,6 +175,29 @@ __device__ __forceinline__ bool not_finite16(uint32_t x) {
     constexpr uint32_t E = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
     return (x & E) == E;
 }
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t x, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
 // bits [lo, hi) of a 32-bit word, bounds clamped
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
     const uint32_t a = lo <= 0 ? 0xffffffffu : lo >= 32 ? 0u : 0xffffffffu << lo;
@@ -225,6 +250,8 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
         *abort_flag = 1;
     };
 
+    if (warp >= 8) {
+    regs_dec<SF_REGS_ISSUE>();
     if (warp == 8) {
         // ------------------------------------------------------ TMA producer
         if (lane == 0) {
@@ -347,15 +374,13 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                     if (nxt.valid) ++qn;
                 }
                 const bool more = !last || nxt.valid;
-                const SinkItem &nx = last ? nxt.x : cur.x;
-                const int nj = last ? 0 : cur.j + 1;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (!ok) break;
                     ok = issue_pv(cur.x, i, cur.j, kv + 1);
                     if (ok && last && begun[i]) tc::mma_commit(o_full + i);
                     if (ok && i == 1) tc::mma_commit(kv_empty + (kv + 1) % SF_SLOTS);
-                    if (ok && more) ok = issue_s(nx, i, nj, kv + 2);
+                    if (ok && more) ok = last ? issue_s(nxt.x, i, 0, kv + 2) : issue_s(cur.x, i, cur.j + 1, kv + 2);
                 }
                 if (!ok) break;
                 if (more) tc::mma_commit(kv_empty + (kv + 2) % SF_SLOTS);
@@ -372,7 +397,9 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
             tc::mbar_wait_bounded(drain, 0, ATC_WAIT);
         }
         __syncwarp();
+    }
     } else {
+        regs_inc<SF_REGS_SOFTMAX>();
         // --------------------------------------------- softmax and epilogue
         const int i = warp >> 2, r = (warp & 3) * 32 + lane;      // row tile, row of it
         const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
@@ -453,7 +480,8 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < SF_KT; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+                for (int c = 0; c < SF_KT; c += 2)
+                    mx[(c >> 1) & 3] = fmaxf(fmaxf(mx[(c >> 1) & 3], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
                 const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
                 const bool raise = mt > m + (m == -INFINITY ? 0.f : SF_RAISE);
                 float alpha = 1.f;
@@ -478,23 +506,28 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                 first = false;
                 ++sn;
                 const float nb = m == -INFINITY ? 0.f : -m;
-                float rs[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t nb2 = f2_pack(nb, nb), sc2 = f2_pack(p.scale_log2, p.scale_log2);
+                uint64_t rs[2] = {0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < SF_KT; c += 32) {
                     if (c < n) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const float p0 = ex2_fast(fmaf(__uint_as_float(s[c + e]), p.scale_log2, nb));
-                            const float p1 = ex2_fast(fmaf(__uint_as_float(s[c + e + 1]), p.scale_log2, nb));
-                            rs[e & 2] += p0;
-                            rs[(e & 2) + 1] += p1;
+                            float p0, p1;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])), sc2, nb2),
+                                      p0, p1);
+                            p0 = ex2_fast(p0);
+                            p1 = ex2_fast(p1);
+                            rs[(e >> 1) & 1] = f2_add(rs[(e >> 1) & 1], f2_pack(p0, p1));
                             pk[e / 2] = pack2<T>(p0, p1);
                         }
                         atc::tmem_st16(tS + c / 2, pk);
                     }
                 }
-                l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+                float r0, r1;
+                f2_unpack(f2_add(rs[0], rs[1]), r0, r1);
+                l += r0 + r1;
                 atc::tmem_st_wait();
                 tc::fence_before_sync();
                 atc::arrive(p_full + i);

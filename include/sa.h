@@ -407,7 +407,7 @@ typedef struct sa_sink_shape {
     int32_t dtype;              /* sa_dtype */
     int32_t B, Hq, Hkv, d;
     int32_t window, sinks;      /* window >= 1 (counts the token itself), sinks >= 0 */
-    float scale;
+    float scale;                /* > 0 */
     int64_t Tq, L;              /* dense: per sequence; packed: rows of the batch */
     int64_t q_pos0;             /* dense only */
     int64_t max_q, max_k;       /* packed only: upper bounds of the lengths, 0 = not known */
@@ -448,7 +448,7 @@ typedef struct sa_paged_shape {
     int32_t B, Hq, Hkv, d;
     int32_t page, max_pages;    /* tokens per page, entries per table row */
     int32_t window, sinks;
-    float scale;
+    float scale;                /* > 0 */
     int64_t n_pages;
     int64_t q_stride[2];                     /* batch, head */
     int64_t k_stride[3], v_stride[3];        /* page, slot, head */
