@@ -35,7 +35,7 @@
 namespace sa {
 
 constexpr int SF_KT = 128;               // keys per tile
-constexpr int SF_SLOTS = 5;              // ring of K and V tiles
+constexpr int SF_SLOTS = 4;              // ring of tiles: K, V of even key tiles, K, V of odd ones
 constexpr int SF_THREADS = 384;          // 3 warpgroups; warps 10 and 11 only give their registers away
 // registers a thread: launched with 168 (384 x 168 = 64512); 2 x 208 + 88 = 3 x 168
 constexpr int SF_REGS_SOFTMAX = 208, SF_REGS_ISSUE = 88;
@@ -49,10 +49,11 @@ struct SfSmem {
     static constexpr int TILE = 128 * D * 2;               // Q, K or V tile: D / 64 halves of 128 rows x 128 B
     static constexpr int OFF_Q = 0;                        // A, B
     static constexpr int OFF_KV = OFF_Q + 2 * TILE;
-    static constexpr int OFF_BAR = OFF_KV + SF_SLOTS * TILE;
-    // q_full[2], q_empty[2], kv_full[S], kv_empty[S], s_full[2], p_full[2], pv_done[2], o_full[2], drain
+    static constexpr int OFF_STAGE = OFF_KV + SF_SLOTS * TILE;      // outputs: 32 rows x 128 B per softmax warp
+    static constexpr int OFF_BAR = OFF_STAGE + 8 * 4096;
+    // q_full[2], q_empty[2], kv_full[S], kv_empty[S], s_full[2], p_full[2][2], o_full[2], drain
     static constexpr int N_BAR = 4 + 2 * SF_SLOTS + 8 + 1;
-    static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;   // tmem slot, abort flag, dirty flag
+    static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;   // tmem slot, abort flag, dirty flag, tile info[2]
     static constexpr int TOTAL = OFF_MISC + 32;
     static constexpr int ALLOC = TOTAL + 1024;
 };
@@ -69,7 +70,7 @@ struct SinkItem {
     int b, hk, h0, nh;       // h0: first head, nh: heads of the tile that belong to the group
     int t0, nq_i[2];         // first query; queries of A and B
     int band_lo, band_hi, s_end, n_sink, nt;
-    int lo_min[2], hi_max[2], s1_max[2];     // over the rows of A and B
+    int ja[2], jb[2];        // key tiles that A and B use: the sinks' and [ja, jb) (none: nq_i = 0)
     int clean_lo, clean_hi;  // keys of [band_lo, clean_lo) and [clean_hi, band_hi) are not seen by every row
 
     __device__ __forceinline__ void tile(int j, int &k0, int &n) const {
@@ -81,14 +82,8 @@ struct SinkItem {
             n = min(SF_KT, band_hi - k0);
         }
     }
-    // does any row of row tile i see a key of tile j?
     __device__ __forceinline__ bool active(int i, int j) const {
-        if ((i ? nq_i[1] : nq_i[0]) == 0) return false;
-        if (j < n_sink) return true;
-        int k0, n;
-        tile(j, k0, n);
-        return k0 < (i ? hi_max[1] : hi_max[0]) &&
-               (k0 + n > (i ? lo_min[1] : lo_min[0]) || k0 < (i ? s1_max[1] : s1_max[0]));
+        return (i ? nq_i[1] : nq_i[0]) > 0 && (j < n_sink || (j >= (i ? ja[1] : ja[0]) && j < (i ? jb[1] : jb[0])));
     }
 };
 __device__ __forceinline__ bool sink_item(const SinkParams &p, const SinkTiles &tl, long long it, SinkItem &x) {
@@ -124,25 +119,29 @@ __device__ __forceinline__ bool sink_item(const SinkParams &p, const SinkTiles &
     x.s_end = min(p.sinks, lo);
     x.clean_lo = lo;
     x.band_hi = hi;
+    int lo_min[2], hi_max[2], s1_max[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int ta = x.t0 + i * tl.TPT;
-        x.nq_i[i] = min(tl.TPT, x.s.nq - ta);
-        if (x.nq_i[i] <= 0) {
-            x.nq_i[i] = 0;
-            x.lo_min[i] = x.hi_max[i] = x.s1_max[i] = 0;
-            continue;
-        }
+        x.nq_i[i] = max(0, min(tl.TPT, x.s.nq - ta));
+        lo_min[i] = hi_max[i] = s1_max[i] = 0;
+        if (x.nq_i[i] == 0) continue;
         sink_visible(p, x.s.nk, x.s.pos0 + ta, s1, lo, hi);
-        x.lo_min[i] = lo;
+        lo_min[i] = lo;
         sink_visible(p, x.s.nk, x.s.pos0 + ta + x.nq_i[i] - 1, s1, lo, hi);
-        x.hi_max[i] = hi;
-        x.s1_max[i] = s1;
+        hi_max[i] = hi;
+        s1_max[i] = s1;
         x.band_hi = hi;
         x.clean_lo = lo;
     }
     x.n_sink = (x.s_end + SF_KT - 1) / SF_KT;
     x.nt = x.n_sink + (x.band_hi - x.band_lo + SF_KT - 1) / SF_KT;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        // a row that still sees sinks inside the band needs the band from its start
+        x.ja[i] = x.n_sink + (s1_max[i] > x.band_lo ? 0 : max(0, lo_min[i] - x.band_lo) / SF_KT);
+        x.jb[i] = x.n_sink + max(0, hi_max[i] - x.band_lo + SF_KT - 1) / SF_KT;
+    }
     return true;
 }
 
@@ -194,6 +193,16 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+    return ok != 0;
+}
+// a wait of a whole warp, with one verdict
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    return __all_sync(0xffffffffu, atc::wait(bar, parity, abort_flag)) != 0;
+}
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
 template <int N>
@@ -204,6 +213,10 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
     const uint32_t b = hi <= 0 ? 0u : hi >= 32 ? 0xffffffffu : ~(0xffffffffu << hi);
     return a & b;
 }
+
+// What the issuing warp has to know of a key tile, written by the producer
+// beside it: columns / 16, who uses it, where its item begins and ends.
+enum : uint32_t { TI_STEPS = 15u, TI_A = 16u, TI_B = 32u, TI_FIRST = 64u, TI_LAST = 128u, TI_TILE = 256u };
 
 template <typename T, int D>
 __global__ void __launch_bounds__(SF_THREADS, 1)
@@ -217,11 +230,11 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
     unsigned char *smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
     uint64_t *q_full = bars, *q_empty = bars + 2, *kv_full = bars + 4, *kv_empty = kv_full + SF_SLOTS;
-    uint64_t *s_full = kv_empty + SF_SLOTS, *p_full = s_full + 2, *pv_done = p_full + 2, *o_full = pv_done + 2;
-    uint64_t *drain = o_full + 2;
+    uint64_t *s_full = kv_empty + SF_SLOTS, *p_full = s_full + 2, *o_full = p_full + 4, *drain = o_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
     volatile int *dirty = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 8);
+    volatile uint32_t *info_s = reinterpret_cast<volatile uint32_t *>(smem + L::OFF_MISC + 16);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (warp == 9) {
@@ -231,8 +244,8 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(q_full + i, 1); tc::mbar_init(q_empty + i, 1);
-            tc::mbar_init(s_full + i, 1); tc::mbar_init(p_full + i, 128); tc::mbar_init(pv_done + i, 1);
-            tc::mbar_init(o_full + i, 1);
+            tc::mbar_init(s_full + i, 1); tc::mbar_init(o_full + i, 1);
+            tc::mbar_init(p_full + 2 * i, 128); tc::mbar_init(p_full + 2 * i + 1, 128);
         }
         for (int i = 0; i < SF_SLOTS; ++i) { tc::mbar_init(kv_full + i, 1); tc::mbar_init(kv_empty + i, 1); }
         tc::mbar_init(drain, 1);
@@ -251,10 +264,10 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
     };
 
     if (warp >= 8) {
-    regs_dec<SF_REGS_ISSUE>();
-    if (warp == 8) {
-        // ------------------------------------------------------ TMA producer
-        if (lane == 0) {
+        regs_dec<SF_REGS_ISSUE>();
+        if (warp == 8 && lane == 0) {
+            // -------------------------------------------------- TMA producer
+            // ring order K 0, V 0, K 1, V 1, ... over all items' tiles, then an empty K that ends the stream
             bool ok = true;
             int qn = 0, kv = 0;                       // items and ring tiles loaded
             for (long long it = blockIdx.x; it < tl.items && ok; it += gridDim.x) {
@@ -269,23 +282,34 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                                 (int)(x.s.q0 + x.t0 + i * tl.TPT), qb, q_full + i);
                     return true;
                 };
-                auto load_kv = [&](const CUtensorMap *map, int j) -> bool {
-                    const int sl = kv % SF_SLOTS;
-                    if (!atc::wait(kv_empty + sl, ((kv / SF_SLOTS) & 1) ^ 1, abort_flag)) return false;
+                for (int j = 0; j < x.nt && ok; ++j) {
                     int k0, n;
                     x.tile(j, k0, n);
-                    atc::expect_tx(kv_full + sl, L::TILE);
-                    for (int h = 0; h < HALVES; ++h)
-                        load_4d(smem + L::OFF_KV + sl * L::TILE + h * (SF_KT * 128), map, h * 64, x.hk,
-                                (int)(x.s.k0 + k0), qb, kv_full + sl);
-                    ++kv;
-                    return true;
-                };
-                ok = load_q(0) && load_kv(&kmap, 0) && load_q(1);
-                if (!ok) break;
+                    for (int v = 0; v < 2 && ok; ++v, ++kv) {
+                        const int sl = kv % SF_SLOTS;
+                        ok = atc::wait(kv_empty + sl, ((kv / SF_SLOTS) & 1) ^ 1, abort_flag);
+                        if (!ok) break;
+                        if (v == 0)
+                            info_s[sl / 2] = (uint32_t)((n + 15) / 16) | (x.active(0, j) ? TI_A : 0u) |
+                                             (x.active(1, j) ? TI_B : 0u) | (j == 0 ? TI_FIRST : 0u) |
+                                             (j + 1 == x.nt ? TI_LAST : 0u) | TI_TILE;
+                        atc::expect_tx(kv_full + sl, L::TILE);
+                        for (int h = 0; h < HALVES; ++h)
+                            load_4d(smem + L::OFF_KV + sl * L::TILE + h * (SF_KT * 128), v ? &vmap : &kmap, h * 64,
+                                    x.hk, (int)(x.s.k0 + k0), qb, kv_full + sl);
+                        if (j == 0 && v == 0) ok = load_q(0) && load_q(1);
+                    }
+                }
                 ++qn;
-                ok = load_kv(&vmap, 0);
-                for (int j = 1; j < x.nt && ok; ++j) ok = load_kv(&kmap, j) && load_kv(&vmap, j);
+            }
+            if (ok) {
+                const int sl = kv % SF_SLOTS;
+                ok = atc::wait(kv_empty + sl, ((kv / SF_SLOTS) & 1) ^ 1, abort_flag);
+                if (ok) {
+                    info_s[sl / 2] = 0u;
+                    atc::arrive(kv_full + sl);
+                    ++kv;
+                }
             }
             if (!ok) fail();
             // let the copies land before the CTA exits
@@ -294,110 +318,104 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                 const int t = kv - 1 - i;
                 tc::mbar_wait_bounded(kv_full + t % SF_SLOTS, (t / SF_SLOTS) & 1, ATC_WAIT);
             }
-        }
-        __syncwarp();
-    } else if (warp == 9) {
-        // --------------------------------------------------------------- MMA
-        if (lane == 0) {
+        } else if (warp == 9) {
+            // ----------------------------------------------------------- MMA
+            // The whole warp walks the tile stream (uniform control flow and
+            // operands); one lane issues.  Its instructions run one after the
+            // other at their latency, so what it has to know of a tile comes
+            // ready from the producer.
             constexpr uint32_t F = ab_format<T>();
             constexpr uint32_t ID_O = tc::make_idesc(1, F, 128, D) | (1u << 16);    // B (V) MN-major
+            constexpr uint32_t TSTEP = L::TILE >> 4;  // descriptor step between tiles
+            const bool leader = elect_one();
+            const uint64_t qd = atc::desc_sw128(tc::smem_u32(smem + L::OFF_Q), 16, 1024);
+            const uint64_t kd = atc::desc_sw128(tc::smem_u32(smem + L::OFF_KV), 16, 1024);
+            // V: MN-major, 64-column atoms SF_KT * 128 B apart, 8-key groups 1 KB apart
+            const uint64_t vd = atc::desc_sw128(tc::smem_u32(smem + L::OFF_KV), SF_KT * 128, 1024);
             bool ok = true;
-            int qn = 0, kv = 0;                       // items begun (Q), ring tiles
-            int pn[2] = {0, 0};
-            struct Cur { SinkItem x; int j; bool valid; };
-            Cur cur, nxt;
-            long long it = blockIdx.x;
-            auto fetch = [&](Cur &c) {                // the next item that has keys
-                c.valid = false;
-                c.j = 0;
-                for (; it < tl.items; it += gridDim.x)
-                    if (sink_item(p, tl, it, c.x) && c.x.nt > 0) {
-                        c.valid = true;
-                        it += gridDim.x;
-                        return;
-                    }
-            };
-            // S of row tile i for tile j of item x; ring tile ks holds its keys
-            auto issue_s = [&](const SinkItem &x, int i, int j, int ks) -> bool {
-                if (j == 0 && !atc::wait(q_full + i, (qn - 1) & 1, abort_flag)) return false;
-                if (!atc::wait(kv_full + ks % SF_SLOTS, (ks / SF_SLOTS) & 1, abort_flag)) return false;
-                if (x.active(i, j)) {
-                    int k0, n;
-                    x.tile(j, k0, n);
-                    const uint32_t id = tc::make_idesc(1, F, 128, (n + 15) & ~15);
-                    tc::fence_after_sync();
-                    const uint32_t qa = tc::smem_u32(smem + L::OFF_Q + i * L::TILE);
-                    const uint32_t ka = tc::smem_u32(smem + L::OFF_KV + (ks % SF_SLOTS) * L::TILE);
+            uint32_t qpar = 1;                        // parity of the current item's Q
+            uint32_t ppar = 0;                        // parity of p_full of A (bit 0), B (bit 1)
+            uint32_t begun = 0;                       // O of A, B holds a product of the current item
+            // S of row tile i over the key tile in K slot k
+            auto issue_s = [&](int i, uint32_t info, int k) {
+                if (info & (TI_A << i)) {
+                    const uint32_t id = tc::make_idesc(1, F, 128, 0) | ((info & TI_STEPS) << 18);   // N / 8 at bit 17
+                    const uint64_t a = qd + i * TSTEP, b = kd + k * TSTEP;
+                    if (leader) {
 #pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                        const int h = c / 4, kk = c % 4;
-                        tc::mma_bf16(tmem + SF_TM_S + i * 128, atc::desc_sw128(qa + h * (128 * 128) + kk * 32, 16, 1024),
-                                     atc::desc_sw128(ka + h * (SF_KT * 128) + kk * 32, 16, 1024), id, c > 0 ? 1u : 0u);
+                        for (int c = 0; c < D / 16; ++c) {
+                            const int off = ((c / 4) * (128 * 128) + (c % 4) * 32) >> 4;
+                            tc::mma_bf16(tmem + SF_TM_S + i * 128, a + off, b + off, id, c > 0 ? 1u : 0u);
+                        }
+                        tc::mma_commit(s_full + i);
                     }
-                    tc::mma_commit(s_full + i);
                 }
-                if (j == x.nt - 1) tc::mma_commit(q_empty + i);
-                return true;
+                if ((info & TI_LAST) && leader) tc::mma_commit(q_empty + i);
             };
-            bool begun[2] = {false, false};           // O of the current item holds a product
-            auto issue_pv = [&](const SinkItem &x, int i, int j, int vs) -> bool {
-                if (!atc::wait(kv_full + vs % SF_SLOTS, (vs / SF_SLOTS) & 1, abort_flag)) return false;
-                if (!x.active(i, j)) return true;
-                // the softmax warps write an item's first P after they have read the O of the item before
-                if (!atc::wait(p_full + i, pn[i] & 1, abort_flag)) return false;
-                ++pn[i];
-                tc::fence_after_sync();
-                int k0, n;
-                x.tile(j, k0, n);
-                const uint32_t va = tc::smem_u32(smem + L::OFF_KV + (vs % SF_SLOTS) * L::TILE);
-                const int steps = (n + 15) / 16;
-                for (int c = 0; c < steps; ++c)
-                    // V: MN-major, 64-column atoms SF_KT * 128 B apart, 8-key groups 1 KB apart
-                    tc::mma_bf16_ts(tmem + SF_TM_O + i * 128, tmem + SF_TM_S + i * 128 + c * 8,
-                                    atc::desc_sw128(va + c * 2048, SF_KT * 128, 1024), ID_O,
-                                    begun[i] || c > 0 ? 1u : 0u);
-                begun[i] = true;
-                tc::mma_commit(pv_done + i);
-                return true;
-            };
-            fetch(cur);
-            if (cur.valid) {
-                ++qn;
-                ok = issue_s(cur.x, 0, 0, 0) && issue_s(cur.x, 1, 0, 0);
-                if (ok) tc::mma_commit(kv_empty + 0);
+            ok = wait_warp(kv_full + 0, 0, abort_flag);
+            uint32_t info = ok ? info_s[0] : 0u;
+            if (info & TI_TILE) {
+                qpar ^= 1;
+                ok = wait_warp(q_full + 0, qpar, abort_flag) && wait_warp(q_full + 1, qpar, abort_flag);
+                if (ok) {
+                    tc::fence_after_sync();
+                    issue_s(0, info, 0);
+                    issue_s(1, info, 0);
+                    if (leader) tc::mma_commit(kv_empty + 0);
+                }
             }
-            // ring tiles: kv = K of the current tile, kv + 1 = V, kv + 2 = K of the next
-            while (ok && cur.valid) {
-                const bool last = cur.j + 1 == cur.x.nt;
-                if (last) {
-                    fetch(nxt);
-                    if (nxt.valid) ++qn;
-                }
-                const bool more = !last || nxt.valid;
+            uint32_t t = 0;                           // key tile; K of tile t in slot 2 (t & 1), V in the next
+            while (ok && (info & TI_TILE)) {
+                const int vs = 2 * (t & 1) + 1, ks = 2 * ((t + 1) & 1);
+                if (!(ok = wait_warp(kv_full + vs, (t >> 1) & 1, abort_flag) &&
+                           wait_warp(kv_full + ks, ((t + 1) >> 1) & 1, abort_flag)))
+                    break;
+                const uint32_t next = info_s[ks / 2];
+                if (next & TI_FIRST) qpar ^= 1;
+                const uint64_t v = vd + vs * TSTEP;
+                const int steps = info & TI_STEPS;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (!ok) break;
-                    ok = issue_pv(cur.x, i, cur.j, kv + 1);
-                    if (ok && last && begun[i]) tc::mma_commit(o_full + i);
-                    if (ok && i == 1) tc::mma_commit(kv_empty + (kv + 1) % SF_SLOTS);
-                    if (ok && more) ok = last ? issue_s(nxt.x, i, 0, kv + 2) : issue_s(cur.x, i, cur.j + 1, kv + 2);
+                    if (info & (TI_A << i)) {
+                        // P.V in two halves, so the first runs while the second's weights are computed; the
+                        // softmax warps write an item's first P after they have read the O of the item before
+                        const uint32_t o = tmem + SF_TM_O + i * 128, pt = tmem + SF_TM_S + i * 128;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!(ok = wait_warp(p_full + 2 * i + h, (ppar >> i) & 1, abort_flag))) break;
+                            tc::fence_after_sync();
+                            if (leader) {
+#pragma unroll
+                                for (int c = 4 * h; c < 4 * h + 4; ++c)
+                                    if (c < steps)
+                                        tc::mma_bf16_ts(o, pt + c * 8, v + c * 128, ID_O, c > 0 ? 1u : (begun >> i) & 1);
+                            }
+                        }
+                        if (!ok) break;
+                        ppar ^= 1u << i;
+                        begun |= 1u << i;
+                    }
+                    if ((info & TI_LAST) && ((begun >> i) & 1) && leader) tc::mma_commit(o_full + i);
+                    if (i == 1 && leader) tc::mma_commit(kv_empty + vs);
+                    if (next & TI_FIRST) {
+                        if (!(ok = wait_warp(q_full + i, qpar, abort_flag))) break;
+                        tc::fence_after_sync();
+                    }
+                    issue_s(i, next, ks);
                 }
                 if (!ok) break;
-                if (more) tc::mma_commit(kv_empty + (kv + 2) % SF_SLOTS);
-                kv += 2;
-                if (last) {
-                    begun[0] = begun[1] = false;
-                    cur = nxt;
-                } else {
-                    ++cur.j;
-                }
+                if ((next & TI_TILE) && leader) tc::mma_commit(kv_empty + ks);
+                if (info & TI_LAST) begun = 0;
+                info = next;
+                ++t;
             }
-            if (!ok) fail();
-            tc::mma_commit(drain);
-            tc::mbar_wait_bounded(drain, 0, ATC_WAIT);
+            if (lane == 0 && !ok) fail();
+            if (leader) {
+                tc::mma_commit(drain);
+                tc::mbar_wait_bounded(drain, 0, ATC_WAIT);
+            }
         }
         __syncwarp();
-    }
     } else {
         regs_inc<SF_REGS_SOFTMAX>();
         // --------------------------------------------- softmax and epilogue
@@ -405,38 +423,41 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
         const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lrow + SF_TM_S + i * 128, tO = tmem + lrow + SF_TM_O + i * 128;
         const int tt = r / tl.HB, hh = r - tt * tl.HB;
-        auto agree = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
+        unsigned char *stage = smem + L::OFF_STAGE + warp * 4096;
         bool ok = true;
-        int sn = 0, on = 0, kv = 0;                   // S tiles, items with an O, ring tiles before this item
+        uint32_t spar = 0, opar = 0;                  // parities of s_full, o_full
+        uint32_t kt0 = 0;                             // key tiles of the stream before this item
         for (long long it = blockIdx.x; it < tl.items && ok; it += gridDim.x) {
             SinkItem x;
             if (!sink_item(p, tl, it, x)) continue;
+            const int nqi = i ? x.nq_i[1] : x.nq_i[0], ja = i ? x.ja[1] : x.ja[0], jb = i ? x.jb[1] : x.jb[0];
             const int t = x.t0 + i * tl.TPT + tt;
-            const bool row_ok = tt < x.nq_i[i] && hh < x.nh;
+            const bool row_ok = tt < nqi && hh < x.nh;
             int s1 = 0, lo = -(1 << 30), hi = 1 << 30;    // rows of nobody: anything, never written
             if (row_ok) sink_visible(p, x.s.nk, x.s.pos0 + t, s1, lo, hi);
             float m = -INFINITY, l = 0.f;
             bool first = true;
-            for (int j = 0; j < x.nt; ++j) {
-                if (!x.active(i, j)) continue;
+            const int jend = nqi > 0 ? max(jb, x.n_sink) : 0;
+            for (int j = x.n_sink > 0 ? 0 : ja; j < jend; j = j + 1 == x.n_sink ? ja : j + 1) {
+                if (j >= x.n_sink && j >= jb) break;
                 int k0, n;
                 x.tile(j, k0, n);
                 // the first row tile that uses this V tile cleans the rows that not every row sees
                 const bool sink = j < x.n_sink;
                 const int ca = sink ? 0 : min(n, max(0, x.clean_lo - k0)), cb = sink ? n : min(n, max(0, x.clean_hi - k0));
                 const int n16 = (n + 15) & ~15;
-                const bool dirt = ca > 0 || cb < n16;
-                if (dirt && (i == 0 || !x.active(0, j))) {
-                    const int vs = kv + 2 * j + 1, sl = vs % SF_SLOTS;
-                    if (!agree(atc::wait(kv_full + sl, (vs / SF_SLOTS) & 1, abort_flag))) { ok = false; break; }
+                if ((ca > 0 || cb < n16) && (i == 0 || !x.active(0, j))) {
+                    const uint32_t kt = kt0 + j;
+                    const int sl = 2 * (kt & 1) + 1;
+                    if (!wait_warp(kv_full + sl, (kt >> 1) & 1, abort_flag)) { ok = false; break; }
                     // 16-byte units of the rows [0, ca) and [cb, n16)
                     constexpr int U = D / 8;
-                    const int rows = ca + (n16 - max(cb, ca));
+                    const int gap = max(cb, ca) - ca, rows = n16 - gap;
                     bool found = false;
                     for (int u = r; u < rows * U; u += 128) {
                         int key = u / U;
                         const int c = u % U;
-                        if (key >= ca) key += max(cb, ca) - ca;
+                        if (key >= ca) key += gap;
                         uint4 *at = reinterpret_cast<uint4 *>(smem + L::OFF_KV + sl * L::TILE + (c / 8) * (SF_KT * 128) +
                                                               key * 128 + (((c & 7) ^ (key & 7)) * 16));
                         if (key >= n) {
@@ -444,7 +465,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                             continue;
                         }
                         uint4 v = *at;
-                        uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+                        uint32_t w[4] = {v.x, v.y, v.z, v.w};
                         bool bad = false;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -452,36 +473,40 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                             if (not_finite16<T>(w[e] >> 16)) { w[e] &= 0xffffu; bad = true; }
                         }
                         if (bad) {
-                            *at = v;
+                            *at = make_uint4(w[0], w[1], w[2], w[3]);
                             found = true;
                         }
                     }
                     if (found) *dirty = 1;
                     tc::fence_proxy_async_smem();
                 }
-                if (!agree(atc::wait(s_full + i, sn & 1, abort_flag))) { ok = false; break; }
+                // S of this tile; P.V of the tile before it was issued earlier and is done with it
+                if (!wait_warp(s_full + i, spar, abort_flag)) { ok = false; break; }
+                spar ^= 1;
                 tc::fence_after_sync();
                 uint32_t s[SF_KT];
 #pragma unroll
                 for (int c = 0; c < SF_KT; c += 32)
                     if (c < n) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(s + c));
                 tc::tmem_ld_wait();
-                const bool whole = n == SF_KT && ((k0 >= lo && k0 + n <= hi) || k0 + n <= s1);
-                if (!__all_sync(0xffffffffu, whole)) {
-#pragma unroll
-                    for (int c = 0; c < SF_KT; c += 32) {
-                        const uint32_t vis = c < n ? (bit_range(lo - k0 - c, hi - k0 - c) | bit_range(0, s1 - k0 - c)) &
-                                                         bit_range(0, n - c)
-                                                   : 0u;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((vis >> e) & 1u)) s[c + e] = __float_as_uint(-INFINITY);
-                    }
-                }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < SF_KT; c += 2)
-                    mx[(c >> 1) & 3] = fmaxf(fmaxf(mx[(c >> 1) & 3], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
+                for (int c = 0; c < SF_KT; c += 32) {
+                    if (c < n) {
+                        const int k = k0 + c;
+                        const bool whole = c + 32 <= n && ((k >= lo && k + 32 <= hi) || k + 32 <= s1);
+                        if (!__all_sync(0xffffffffu, whole)) {
+                            const uint32_t vis = (bit_range(lo - k, hi - k) | bit_range(0, s1 - k)) & bit_range(0, n - c);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!((vis >> e) & 1u)) s[c + e] = __float_as_uint(-INFINITY);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            mx[(e >> 1) & 3] = fmaxf(fmaxf(mx[(e >> 1) & 3], __uint_as_float(s[c + e])),
+                                                     __uint_as_float(s[c + e + 1]));
+                    }
+                }
                 const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
                 const bool raise = mt > m + (m == -INFINITY ? 0.f : SF_RAISE);
                 float alpha = 1.f;
@@ -491,9 +516,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                     l *= alpha;
                 }
                 if (!first && __any_sync(0xffffffffu, raise)) {
-                    if (!agree(atc::wait(pv_done + i, (sn - 1) & 1, abort_flag))) { ok = false; break; }
-                    tc::fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
                         uint32_t o16[16];
                         tc::tmem_ld16(tO + c, o16);
@@ -504,7 +527,6 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                     }
                 }
                 first = false;
-                ++sn;
                 const float nb = m == -INFINITY ? 0.f : -m;
                 const uint64_t nb2 = f2_pack(nb, nb), sc2 = f2_pack(p.scale_log2, p.scale_log2);
                 uint64_t rs[2] = {0ull, 0ull};
@@ -524,62 +546,83 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                         }
                         atc::tmem_st16(tS + c / 2, pk);
                     }
+                    if (c == 32 || c == 96) {         // a half of P is in place
+                        atc::tmem_st_wait();
+                        tc::fence_before_sync();
+                        atc::arrive(p_full + 2 * i + c / 64);
+                    }
                 }
                 float r0, r1;
                 f2_unpack(f2_add(rs[0], rs[1]), r0, r1);
                 l += r0 + r1;
-                atc::tmem_st_wait();
-                tc::fence_before_sync();
-                atc::arrive(p_full + i);
             }
             if (!ok) break;
+            kt0 += x.nt;
             // ------------------------------------------------------ epilogue
-            const long long orow = ((p.cu_q ? 0 : (long long)x.b * p.Tq) + x.s.q0 + t) * p.Hq + x.h0 + hh;
+            if (nqi == 0) continue;
+            const long long row0 = (p.cu_q ? 0 : (long long)x.b * p.Tq) + x.s.q0 + x.t0 + i * tl.TPT;
             if (!first) {
-                if (!agree(atc::wait(o_full + i, on & 1, abort_flag))) { ok = false; break; }
+                if (!wait_warp(o_full + i, opar, abort_flag)) { ok = false; break; }
+                opar ^= 1;
                 tc::fence_after_sync();
-                ++on;
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const bool patch = *dirty != 0;            // set once, for every later item of this CTA
+            const bool patch = *dirty != 0;           // set once, for every later item of this CTA
+            // 64 columns at a time through the warp's own shared memory, so that whole lines are written
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 64) {
 #pragma unroll
-            for (int c = 0; c < D; c += 16) {
-                uint32_t o16[16];
-                if (first) {                          // no key tile: O holds nothing of this item
+                for (int c = 0; c < 64; c += 32) {
+                    uint32_t o[32];
+                    if (first) {                      // no key tile: O holds nothing of this item
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o16[e] = 0u;
-                } else {
-                    tc::tmem_ld16(tO + c, o16);
-                    tc::tmem_ld_wait();
-                }
-                if (row_ok) {
-                    float f[16];
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    } else {
+                        tmem_ld32(tO + c0 + c, o);
+                        tc::tmem_ld_wait();
+                    }
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = l == 0.f ? 0.f : __uint_as_float(o16[e]) * inv;
-                    if (patch) {
+                    for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
+                    if (patch && row_ok) {
                         const T *vb = (const T *)p.v + (p.cu_q ? 0 : x.b) * p.v_s[0] + x.s.k0 * p.v_s[1] +
-                                      x.hk * p.v_s[2] + c;
+                                      x.hk * p.v_s[2] + c0 + c;
+#pragma unroll 1
                         for (int k = x.band_lo; k < x.band_hi; ++k) {
                             if (k == x.clean_lo && k < x.clean_hi) k = x.clean_hi;
                             if (k >= x.band_hi) break;
                             if (!(k < s1 || (k >= lo && k < hi))) continue;
-                            for (int e = 0; e < 16; ++e) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
                                 const float v = to_f(vb[k * p.v_s[1] + e]);
-                                if (!isfinite(v)) f[e] += v;
+                                if (!isfinite(v)) o[e] = __float_as_uint(__uint_as_float(o[e]) + v);
                             }
                         }
                     }
-                    uint32_t w[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = pack2<T>(f[2 * e], f[2 * e + 1]);
-                    uint4 *dst = reinterpret_cast<uint4 *>((T *)p.out + orow * D + c);
-                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    for (int u = 0; u < 4; ++u) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack2<T>(__uint_as_float(o[8 * u + 2 * e]), __uint_as_float(o[8 * u + 2 * e + 1]));
+                        *reinterpret_cast<uint4 *>(stage + lane * 128 + (((c / 8 + u) ^ (lane & 7)) * 16)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
                 }
+                __syncwarp();
+                // 8 lanes per row, 4 rows at a time
+                const uint32_t good = __ballot_sync(0xffffffffu, row_ok);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int rr = k * 4 + lane / 8, u = lane % 8, ro = (warp & 3) * 32 + rr;
+                    const int rt = ro / tl.HB, rh = ro - rt * tl.HB;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((u ^ (rr & 7)) * 16));
+                    if ((good >> rr) & 1)
+                        *reinterpret_cast<uint4 *>((T *)p.out + ((row0 + rt) * p.Hq + x.h0 + rh) * D + c0 + u * 8) = v;
+                }
+                __syncwarp();
             }
-            if (row_ok) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (row_ok) p.lse[(row0 + tt) * p.Hq + x.h0 + hh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             tc::fence_before_sync();
-            kv += 2 * x.nt;
         }
         if (!ok) fail();
     }
