@@ -30,7 +30,10 @@ static int sink_check(const char *what, const sa_sink_shape *s, const void *q, c
     // positions, row numbers and key tiles are 32-bit
     if (s->Tq >= INT_MAX / 2 || s->L >= INT_MAX / 2 || s->q_pos0 >= INT_MAX / 2)
         return fail(SA_ERR_UNSUPPORTED, "%s: lengths above 2^30", what);
-    if ((long long)s->B * s->Tq * s->Hq >= (1ll << 40) || (long long)s->B * s->L * s->Hkv >= (1ll << 40))
+    // so are the work items: at most one per query, KV head and 128 heads of its group, and one more per sequence
+    // (a step beyond the last may be formed)
+    if (((cu_q ? 1ll : s->B) * s->Tq + s->B) * s->Hkv * ((s->Hq / s->Hkv + 127) / 128) >= INT_MAX / 2 ||
+        (long long)s->Hq >= (1 << 20))
         return fail(SA_ERR_UNSUPPORTED, "%s: too many rows", what);
     if ((cu_q == nullptr) != (cu_k == nullptr)) return fail(SA_ERR_INVALID_ARG, "%s: cu_q and cu_k go together", what);
     const bool no_q = s->Tq == 0, no_k = s->L == 0;       // an empty tensor may have a null pointer
@@ -99,8 +102,8 @@ static SinkTiles sink_tiles(const SinkParams &p) {
     t.HC = (p.G + 127) / 128;
     t.TPT = 128 / t.HB;
     const long long TI = 2 * t.TPT;
-    t.blocks = p.cu_q ? p.Tq / TI + p.B : p.B * ((p.Tq + TI - 1) / TI);
-    t.items = t.blocks * p.Hkv * t.HC;
+    t.per_seq = (int)((p.Tq + TI - 1) / TI);
+    t.items = (int)((p.cu_q ? p.Tq / TI + p.B : (long long)p.B * t.per_seq) * p.Hkv * t.HC);
     return t;
 }
 

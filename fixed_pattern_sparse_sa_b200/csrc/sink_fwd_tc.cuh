@@ -14,8 +14,8 @@
 // rounded to the inputs' type (half a step a weight, as the output is).
 //
 // The tensor cores and the softmax alternate between A and B: while one
-// tile's scores are turned into weights the other's products run.  Queue
-// order: P.V of A(j), S of A(j+1), P.V of B(j), S of B(j+1), across items.
+// tile's scores are turned into weights the other's products run.  Each row
+// tile's queue is S(0), then P.V(j), S(j+1), ..., across items.
 // A tile of n < 128 keys costs N = n (rounded up to 16) columns in the first
 // product and n rows in the second, so short sinks and window ends are cheap;
 // a row tile skips key tiles that none of its rows sees.
@@ -25,7 +25,7 @@
 // finite there is added back, at the end, to the rows that do see it.
 //
 // Warps: 0-3 softmax and epilogue of A (thread = row), 4-7 of B, 8 TMA
-// producer, 9 MMA issuer and TMEM owner.  Every wait is bounded; a timeout
+// producer, 9 and 10 MMA issuers of A and B (9 also owns the TMEM).  Every wait is bounded; a timeout
 // sets ERR_TIMEOUT and the CTA drains and exits.
 #pragma once
 
@@ -36,7 +36,7 @@ namespace sa {
 
 constexpr int SF_KT = 128;               // keys per tile
 constexpr int SF_SLOTS = 4;              // ring of tiles: K, V of even key tiles, K, V of odd ones
-constexpr int SF_THREADS = 384;          // 3 warpgroups; warps 10 and 11 only give their registers away
+constexpr int SF_THREADS = 384;          // 3 warpgroups; warp 11 only gives its registers away
 // registers a thread: launched with 168 (384 x 168 = 64512); 2 x 208 + 88 = 3 x 168
 constexpr int SF_REGS_SOFTMAX = 208, SF_REGS_ISSUE = 88;
 constexpr uint32_t SF_TM_S = 0;          // S / P of A, B: 128 columns each
@@ -51,17 +51,19 @@ struct SfSmem {
     static constexpr int OFF_KV = OFF_Q + 2 * TILE;
     static constexpr int OFF_STAGE = OFF_KV + SF_SLOTS * TILE;      // outputs: 32 rows x 128 B per softmax warp
     static constexpr int OFF_BAR = OFF_STAGE + 8 * 4096;
-    // q_full[2], q_empty[2], kv_full[S], kv_empty[S], s_full[2], p_full[2][2], o_full[2], drain
-    static constexpr int N_BAR = 4 + 2 * SF_SLOTS + 8 + 1;
+    // q_full[2], q_empty[2], kv_full[S], kv_empty[S], s_full[2], p_full[2][2], o_full[2], drain[2],
+    // item_full[2], item_empty[2]
+    static constexpr int N_BAR = 4 + 2 * SF_SLOTS + 8 + 2 + 4;
     static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;   // tmem slot, abort flag, dirty flag, tile info[2]
-    static constexpr int TOTAL = OFF_MISC + 32;
+    static constexpr int OFF_ITEM = OFF_MISC + 32;         // two work items of the softmax warps
+    static constexpr int TOTAL = OFF_ITEM + 2 * 64;
     static constexpr int ALLOC = TOTAL + 1024;
 };
 
 struct SinkTiles {
     int HB, HC, TPT;         // heads per row tile, head chunks per group, queries per row tile
-    long long blocks;        // query blocks of 2 * TPT over the batch (packed: an upper bound)
-    long long items;         // blocks * Hkv * HC
+    int per_seq;             // dense: query blocks of 2 * TPT per sequence
+    int items;               // query blocks (packed: an upper bound) * Hkv * HC
 };
 
 // One work item: its sequence, rows and key tiles.
@@ -86,32 +88,31 @@ struct SinkItem {
         return (i ? nq_i[1] : nq_i[0]) > 0 && (j < n_sink || (j >= (i ? ja[1] : ja[0]) && j < (i ? jb[1] : jb[0])));
     }
 };
-__device__ __forceinline__ bool sink_item(const SinkParams &p, const SinkTiles &tl, long long it, SinkItem &x) {
-    const int hh = (int)(it % (p.Hkv * tl.HC));
-    const long long blk = it / (p.Hkv * tl.HC);
-    x.hk = hh / tl.HC;
-    const int hc = hh % tl.HC, TI = 2 * tl.TPT;
+__device__ __forceinline__ bool sink_item(const SinkParams &p, const SinkTiles &tl, int it, SinkItem &x) {
+    const int H2 = p.Hkv * tl.HC, blk = it / H2, hh = it - blk * H2;
+    const int hc = tl.HC == 1 ? 0 : hh % tl.HC;
+    const unsigned TI = 2 * tl.TPT;
+    x.hk = tl.HC == 1 ? hh : hh / tl.HC;
     x.h0 = x.hk * p.G + hc * tl.HB;
     x.nh = min(tl.HB, p.G - hc * tl.HB);
-    long long local;
+    int local;
     if (!p.cu_q) {
-        const long long per = (p.Tq + TI - 1) / TI;
-        x.b = (int)(blk / per);
-        local = blk % per;
+        x.b = blk / tl.per_seq;
+        local = blk - x.b * tl.per_seq;
     } else {
         // sequence b starts at block cu[b] / TI + b: the last start at or before blk
         int lo = 0, hi = p.B;
         while (hi - lo > 1) {
             const int m = (lo + hi) / 2;
-            const long long c = min(max((long long)__ldg(p.cu_q + m), 0ll), p.Tq);
-            if (c / TI + m <= blk) lo = m; else hi = m;
+            const unsigned c = (unsigned)min(max(__ldg(p.cu_q + m), 0), (int)p.Tq);
+            if ((long long)(c / TI) + m <= blk) lo = m; else hi = m;
         }
         x.b = lo;
-        local = blk - (min(max((long long)__ldg(p.cu_q + lo), 0ll), p.Tq) / TI + lo);
+        local = blk - (int)((unsigned)min(max(__ldg(p.cu_q + lo), 0), (int)p.Tq) / TI + lo);
     }
     x.s = sink_seq(p, x.b);
-    if (local < 0 || local * TI >= x.s.nq) return false;
-    x.t0 = (int)(local * TI);
+    if (local < 0 || (long long)local * TI >= x.s.nq) return false;
+    x.t0 = local * TI;
     int s1, lo, hi;
     sink_visible(p, x.s.nk, x.s.pos0 + x.t0, s1, lo, hi);
     x.band_lo = lo;
@@ -188,6 +189,16 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -214,6 +225,17 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
     return a & b;
 }
 
+// What the softmax warps have to know of a work item (16 words).
+struct alignas(16) SfItem {
+    int nt;                  // key tiles; -1 ends the stream
+    int nq[2];               // queries of A and B
+    int pos;                 // position of the first query
+    int band_lo, band_hi, s_end, n_sink;
+    int ja[2], jb[2];
+    int clean_lo, clean_hi;
+    int heads;               // first head | heads of the tile << 20
+    int row;                 // first query's row of the whole batch
+};
 // What the issuing warp has to know of a key tile, written by the producer
 // beside it: columns / 16, who uses it, where its item begins and ends.
 enum : uint32_t { TI_STEPS = 15u, TI_A = 16u, TI_B = 32u, TI_FIRST = 64u, TI_LAST = 128u, TI_TILE = 256u };
@@ -231,6 +253,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
     uint64_t *q_full = bars, *q_empty = bars + 2, *kv_full = bars + 4, *kv_empty = kv_full + SF_SLOTS;
     uint64_t *s_full = kv_empty + SF_SLOTS, *p_full = s_full + 2, *o_full = p_full + 4, *drain = o_full + 2;
+    uint64_t *item_full = drain + 2, *item_empty = item_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
     volatile int *dirty = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 8);
@@ -246,9 +269,10 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
             tc::mbar_init(q_full + i, 1); tc::mbar_init(q_empty + i, 1);
             tc::mbar_init(s_full + i, 1); tc::mbar_init(o_full + i, 1);
             tc::mbar_init(p_full + 2 * i, 128); tc::mbar_init(p_full + 2 * i + 1, 128);
+            tc::mbar_init(drain + i, 1);
+            tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 256);
         }
-        for (int i = 0; i < SF_SLOTS; ++i) { tc::mbar_init(kv_full + i, 1); tc::mbar_init(kv_empty + i, 1); }
-        tc::mbar_init(drain, 1);
+        for (int i = 0; i < SF_SLOTS; ++i) { tc::mbar_init(kv_full + i, 1); tc::mbar_init(kv_empty + i, 2); }
         *abort_flag = 0;
         *dirty = 0;
         tc::mbar_fence_init();
@@ -263,16 +287,125 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
         *abort_flag = 1;
     };
 
+    // ------------------------------------------------------------------- MMA
+    // One warp per row tile walks the tile stream (uniform control flow and
+    // operands); one lane issues.  Its instructions run one after the other at
+    // their latency, so what it has to know of a tile comes ready from the
+    // producer, and two warps share the issuing.
+    auto issue = [&](auto which) {
+        constexpr int I = decltype(which)::value;
+        constexpr uint32_t F = ab_format<T>();
+        constexpr uint32_t ID_O = tc::make_idesc(1, F, 128, D) | (1u << 16);    // B (V) MN-major
+        constexpr uint32_t TSTEP = L::TILE >> 4;      // descriptor step between tiles
+        constexpr uint32_t USES = I == 0 ? TI_A : TI_B;
+        const bool leader = elect_one();
+        const uint64_t qd = atc::desc_sw128(tc::smem_u32(smem + L::OFF_Q + I * L::TILE), 16, 1024);
+        const uint64_t kd = atc::desc_sw128(tc::smem_u32(smem + L::OFF_KV), 16, 1024);
+        // V: MN-major, 64-column atoms SF_KT * 128 B apart, 8-key groups 1 KB apart
+        const uint64_t vd = atc::desc_sw128(tc::smem_u32(smem + L::OFF_KV), SF_KT * 128, 1024);
+        const uint32_t tS = tmem + SF_TM_S + I * 128, tO = tmem + SF_TM_O + I * 128;
+        bool ok = true;
+        uint32_t qpar = 1, ppar = 0;                  // parities of the current item's Q, of P
+        uint32_t begun = 0;                           // O holds a product of the current item
+        // S over the key tile in K slot k
+        auto issue_s = [&](uint32_t info, int k) {
+            if (leader) {
+                if (info & USES) {
+                    const uint32_t id = tc::make_idesc(1, F, 128, 0) | ((info & TI_STEPS) << 18);   // N / 8 at bit 17
+                    const uint64_t b = kd + k * TSTEP;
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        const int off = ((c / 4) * (128 * 128) + (c % 4) * 32) >> 4;
+                        tc::mma_bf16(tS, qd + off, b + off, id, c > 0 ? 1u : 0u);
+                    }
+                    tc::mma_commit(s_full + I);
+                }
+                if (info & TI_LAST) tc::mma_commit(q_empty + I);
+                if (info & TI_TILE) tc::mma_commit(kv_empty + k);
+            }
+        };
+        ok = wait_warp(kv_full + 0, 0, abort_flag);
+        uint32_t info = ok ? info_s[0] : 0u;
+        if (info & TI_TILE) {
+            qpar ^= 1;
+            ok = wait_warp(q_full + I, qpar, abort_flag);
+            if (ok) {
+                tc::fence_after_sync();
+                issue_s(info, 0);
+            }
+        }
+        uint32_t t = 0;                               // key tile; K of tile t in slot 2 (t & 1), V in the next
+        while (ok && (info & TI_TILE)) {
+            const int vs = 2 * (t & 1) + 1, ks = 2 * ((t + 1) & 1);
+            if (!(ok = wait_warp(kv_full + vs, (t >> 1) & 1, abort_flag) &&
+                       wait_warp(kv_full + ks, ((t + 1) >> 1) & 1, abort_flag)))
+                break;
+            const uint32_t next = info_s[ks / 2];
+            if (next & TI_FIRST) {
+                qpar ^= 1;
+                if (!(ok = wait_warp(q_full + I, qpar, abort_flag))) break;
+            }
+            if (info & USES) {
+                // P.V in two halves, so the first runs while the second's weights are computed; the
+                // softmax warps write an item's first P after they have read the O of the item before
+                const uint64_t v = vd + vs * TSTEP;
+                const int steps = info & TI_STEPS;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!(ok = wait_warp(p_full + 2 * I + h, ppar, abort_flag))) break;
+                    tc::fence_after_sync();
+                    if (leader) {
+#pragma unroll
+                        for (int c = 4 * h; c < 4 * h + 4; ++c)
+                            if (c < steps) tc::mma_bf16_ts(tO, tS + c * 8, v + c * 128, ID_O, c > 0 ? 1u : begun);
+                    }
+                }
+                if (!ok) break;
+                ppar ^= 1;
+                begun = 1;
+            }
+            if (leader) {
+                if ((info & TI_LAST) && begun) tc::mma_commit(o_full + I);
+                tc::mma_commit(kv_empty + vs);
+            }
+            issue_s(next, ks);
+            if (info & TI_LAST) begun = 0;
+            info = next;
+            ++t;
+        }
+        if (lane == 0 && !ok) fail();
+        if (leader) {
+            tc::mma_commit(drain + I);
+            tc::mbar_wait_bounded(drain + I, 0, ATC_WAIT);
+        }
+    };
+
     if (warp >= 8) {
         regs_dec<SF_REGS_ISSUE>();
         if (warp == 8 && lane == 0) {
             // -------------------------------------------------- TMA producer
             // ring order K 0, V 0, K 1, V 1, ... over all items' tiles, then an empty K that ends the stream
             bool ok = true;
-            int qn = 0, kv = 0;                       // items and ring tiles loaded
-            for (long long it = blockIdx.x; it < tl.items && ok; it += gridDim.x) {
+            int qn = 0, kv = 0, in = 0;               // items with keys and ring tiles loaded, items handed over
+            auto hand_over = [&](const SfItem &y) -> bool {
+                if (!atc::wait(item_empty + (in & 1), ((in >> 1) & 1) ^ 1, abort_flag)) return false;
+                const int4 *src = reinterpret_cast<const int4 *>(&y);
+                int4 *dst = reinterpret_cast<int4 *>(smem + L::OFF_ITEM + (in & 1) * sizeof(SfItem));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) dst[c] = src[c];
+                atc::arrive(item_full + (in & 1));
+                ++in;
+                return true;
+            };
+            for (int it = blockIdx.x; it < tl.items && ok; it += gridDim.x) {
                 SinkItem x;
-                if (!sink_item(p, tl, it, x) || x.nt == 0) continue;
+                if (!sink_item(p, tl, it, x)) continue;
+                ok = hand_over(SfItem{x.nt, {x.nq_i[0], x.nq_i[1]}, (int)x.s.pos0 + x.t0, x.band_lo, x.band_hi, x.s_end,
+                                      x.n_sink, {x.ja[0], x.ja[1]}, {x.jb[0], x.jb[1]}, x.clean_lo, x.clean_hi,
+                                      x.h0 | x.nh << 20,
+                                      (int)((p.cu_q ? 0 : x.b * p.Tq) + x.s.q0) + x.t0});
+                if (!ok) break;
+                if (x.nt == 0) continue;
                 const int qb = p.cu_q ? 0 : x.b;
                 auto load_q = [&](int i) -> bool {
                     if (!atc::wait(q_empty + i, (qn & 1) ^ 1, abort_flag)) return false;
@@ -305,6 +438,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
             if (ok) {
                 const int sl = kv % SF_SLOTS;
                 ok = atc::wait(kv_empty + sl, ((kv / SF_SLOTS) & 1) ^ 1, abort_flag);
+                if (ok) ok = hand_over(SfItem{-1});
                 if (ok) {
                     info_s[sl / 2] = 0u;
                     atc::arrive(kv_full + sl);
@@ -319,101 +453,9 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                 tc::mbar_wait_bounded(kv_full + t % SF_SLOTS, (t / SF_SLOTS) & 1, ATC_WAIT);
             }
         } else if (warp == 9) {
-            // ----------------------------------------------------------- MMA
-            // The whole warp walks the tile stream (uniform control flow and
-            // operands); one lane issues.  Its instructions run one after the
-            // other at their latency, so what it has to know of a tile comes
-            // ready from the producer.
-            constexpr uint32_t F = ab_format<T>();
-            constexpr uint32_t ID_O = tc::make_idesc(1, F, 128, D) | (1u << 16);    // B (V) MN-major
-            constexpr uint32_t TSTEP = L::TILE >> 4;  // descriptor step between tiles
-            const bool leader = elect_one();
-            const uint64_t qd = atc::desc_sw128(tc::smem_u32(smem + L::OFF_Q), 16, 1024);
-            const uint64_t kd = atc::desc_sw128(tc::smem_u32(smem + L::OFF_KV), 16, 1024);
-            // V: MN-major, 64-column atoms SF_KT * 128 B apart, 8-key groups 1 KB apart
-            const uint64_t vd = atc::desc_sw128(tc::smem_u32(smem + L::OFF_KV), SF_KT * 128, 1024);
-            bool ok = true;
-            uint32_t qpar = 1;                        // parity of the current item's Q
-            uint32_t ppar = 0;                        // parity of p_full of A (bit 0), B (bit 1)
-            uint32_t begun = 0;                       // O of A, B holds a product of the current item
-            // S of row tile i over the key tile in K slot k
-            auto issue_s = [&](int i, uint32_t info, int k) {
-                if (info & (TI_A << i)) {
-                    const uint32_t id = tc::make_idesc(1, F, 128, 0) | ((info & TI_STEPS) << 18);   // N / 8 at bit 17
-                    const uint64_t a = qd + i * TSTEP, b = kd + k * TSTEP;
-                    if (leader) {
-#pragma unroll
-                        for (int c = 0; c < D / 16; ++c) {
-                            const int off = ((c / 4) * (128 * 128) + (c % 4) * 32) >> 4;
-                            tc::mma_bf16(tmem + SF_TM_S + i * 128, a + off, b + off, id, c > 0 ? 1u : 0u);
-                        }
-                        tc::mma_commit(s_full + i);
-                    }
-                }
-                if ((info & TI_LAST) && leader) tc::mma_commit(q_empty + i);
-            };
-            ok = wait_warp(kv_full + 0, 0, abort_flag);
-            uint32_t info = ok ? info_s[0] : 0u;
-            if (info & TI_TILE) {
-                qpar ^= 1;
-                ok = wait_warp(q_full + 0, qpar, abort_flag) && wait_warp(q_full + 1, qpar, abort_flag);
-                if (ok) {
-                    tc::fence_after_sync();
-                    issue_s(0, info, 0);
-                    issue_s(1, info, 0);
-                    if (leader) tc::mma_commit(kv_empty + 0);
-                }
-            }
-            uint32_t t = 0;                           // key tile; K of tile t in slot 2 (t & 1), V in the next
-            while (ok && (info & TI_TILE)) {
-                const int vs = 2 * (t & 1) + 1, ks = 2 * ((t + 1) & 1);
-                if (!(ok = wait_warp(kv_full + vs, (t >> 1) & 1, abort_flag) &&
-                           wait_warp(kv_full + ks, ((t + 1) >> 1) & 1, abort_flag)))
-                    break;
-                const uint32_t next = info_s[ks / 2];
-                if (next & TI_FIRST) qpar ^= 1;
-                const uint64_t v = vd + vs * TSTEP;
-                const int steps = info & TI_STEPS;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (info & (TI_A << i)) {
-                        // P.V in two halves, so the first runs while the second's weights are computed; the
-                        // softmax warps write an item's first P after they have read the O of the item before
-                        const uint32_t o = tmem + SF_TM_O + i * 128, pt = tmem + SF_TM_S + i * 128;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (!(ok = wait_warp(p_full + 2 * i + h, (ppar >> i) & 1, abort_flag))) break;
-                            tc::fence_after_sync();
-                            if (leader) {
-#pragma unroll
-                                for (int c = 4 * h; c < 4 * h + 4; ++c)
-                                    if (c < steps)
-                                        tc::mma_bf16_ts(o, pt + c * 8, v + c * 128, ID_O, c > 0 ? 1u : (begun >> i) & 1);
-                            }
-                        }
-                        if (!ok) break;
-                        ppar ^= 1u << i;
-                        begun |= 1u << i;
-                    }
-                    if ((info & TI_LAST) && ((begun >> i) & 1) && leader) tc::mma_commit(o_full + i);
-                    if (i == 1 && leader) tc::mma_commit(kv_empty + vs);
-                    if (next & TI_FIRST) {
-                        if (!(ok = wait_warp(q_full + i, qpar, abort_flag))) break;
-                        tc::fence_after_sync();
-                    }
-                    issue_s(i, next, ks);
-                }
-                if (!ok) break;
-                if ((next & TI_TILE) && leader) tc::mma_commit(kv_empty + ks);
-                if (info & TI_LAST) begun = 0;
-                info = next;
-                ++t;
-            }
-            if (lane == 0 && !ok) fail();
-            if (leader) {
-                tc::mma_commit(drain);
-                tc::mbar_wait_bounded(drain, 0, ATC_WAIT);
-            }
+            issue(std::integral_constant<int, 0>{});
+        } else if (warp == 10) {
+            issue(std::integral_constant<int, 1>{});
         }
         __syncwarp();
     } else {
@@ -427,33 +469,52 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
         bool ok = true;
         uint32_t spar = 0, opar = 0;                  // parities of s_full, o_full
         uint32_t kt0 = 0;                             // key tiles of the stream before this item
-        for (long long it = blockIdx.x; it < tl.items && ok; it += gridDim.x) {
-            SinkItem x;
-            if (!sink_item(p, tl, it, x)) continue;
-            const int nqi = i ? x.nq_i[1] : x.nq_i[0], ja = i ? x.ja[1] : x.ja[0], jb = i ? x.jb[1] : x.jb[0];
-            const int t = x.t0 + i * tl.TPT + tt;
-            const bool row_ok = tt < nqi && hh < x.nh;
+        for (uint32_t in = 0;; ++in) {
+            if (!wait_warp(item_full + (in & 1), (in >> 1) & 1, abort_flag)) { ok = false; break; }
+            SfItem x;
+            {
+                const int4 *src = reinterpret_cast<const int4 *>(smem + L::OFF_ITEM + (in & 1) * sizeof(SfItem));
+                int4 *dst = reinterpret_cast<int4 *>(&x);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) dst[c] = src[c];
+            }
+            atc::arrive(item_empty + (in & 1));
+            if (x.nt < 0) break;
+            const int nqi = i ? x.nq[1] : x.nq[0], ja = i ? x.ja[1] : x.ja[0], jb = i ? x.jb[1] : x.jb[0];
+            const bool row_ok = tt < nqi && hh < (x.heads >> 20);
             int s1 = 0, lo = -(1 << 30), hi = 1 << 30;    // rows of nobody: anything, never written
-            if (row_ok) sink_visible(p, x.s.nk, x.s.pos0 + t, s1, lo, hi);
+            if (row_ok) {
+                const int pos = x.pos + i * tl.TPT + tt;
+                hi = min(max(pos + 1, 0), x.band_hi);     // the last row of the item sees up to band_hi
+                lo = min(max(pos - p.window + 1, 0), hi);
+                s1 = min(p.sinks, lo);
+            }
             float m = -INFINITY, l = 0.f;
             bool first = true;
-            const int jend = nqi > 0 ? max(jb, x.n_sink) : 0;
-            for (int j = x.n_sink > 0 ? 0 : ja; j < jend; j = j + 1 == x.n_sink ? ja : j + 1) {
-                if (j >= x.n_sink && j >= jb) break;
-                int k0, n;
-                x.tile(j, k0, n);
+            // the sinks' tiles, then [ja, jb): next tile j at key k0, the range's end, the range to clean
+            bool in_sink = x.n_sink > 0;
+            int j = in_sink ? 0 : ja, jend = nqi == 0 ? 0 : in_sink ? x.n_sink : jb;
+            int k0 = in_sink ? 0 : x.band_lo + (ja - x.n_sink) * SF_KT, kend = in_sink ? x.s_end : x.band_hi;
+            int cl = in_sink ? 0 : x.clean_lo, ch = in_sink ? x.s_end : x.clean_hi;
+            if (nqi > 0) for (;; ++j, k0 += SF_KT) {
+                if (j >= jend) {
+                    if (!in_sink || ja >= jb) break;
+                    in_sink = false;
+                    j = ja; jend = jb; k0 = x.band_lo + (ja - x.n_sink) * SF_KT; kend = x.band_hi;
+                    cl = x.clean_lo; ch = x.clean_hi;
+                }
+                const int n = min(SF_KT, kend - k0), n16 = (n + 15) & ~15;
                 // the first row tile that uses this V tile cleans the rows that not every row sees
-                const bool sink = j < x.n_sink;
-                const int ca = sink ? 0 : min(n, max(0, x.clean_lo - k0)), cb = sink ? n : min(n, max(0, x.clean_hi - k0));
-                const int n16 = (n + 15) & ~15;
-                if ((ca > 0 || cb < n16) && (i == 0 || !x.active(0, j))) {
+                if ((k0 < cl || k0 + n16 > ch) &&
+                    (i == 0 || !(x.nq[0] > 0 && (in_sink || (j >= x.ja[0] && j < x.jb[0]))))) {
                     const uint32_t kt = kt0 + j;
-                    const int sl = 2 * (kt & 1) + 1;
+                    const int sl = 2 * (kt & 1) + 1, ca = min(n, max(0, cl - k0)), cb = min(n, max(0, ch - k0));
                     if (!wait_warp(kv_full + sl, (kt >> 1) & 1, abort_flag)) { ok = false; break; }
                     // 16-byte units of the rows [0, ca) and [cb, n16)
                     constexpr int U = D / 8;
                     const int gap = max(cb, ca) - ca, rows = n16 - gap;
                     bool found = false;
+#pragma unroll 1
                     for (int u = r; u < rows * U; u += 128) {
                         int key = u / U;
                         const int c = u % U;
@@ -490,22 +551,29 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                     if (c < n) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(s + c));
                 tc::tmem_ld_wait();
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto chunk_max = [&](int c) {
 #pragma unroll
-                for (int c = 0; c < SF_KT; c += 32) {
-                    if (c < n) {
-                        const int k = k0 + c;
-                        const bool whole = c + 32 <= n && ((k >= lo && k + 32 <= hi) || k + 32 <= s1);
-                        if (!__all_sync(0xffffffffu, whole)) {
+                    for (int e = 0; e < 32; e += 2)
+                        mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(s[c + e]),
+                                                __uint_as_float(s[c + e + 1]));
+                };
+                const bool whole = n == SF_KT && ((k0 >= lo && k0 + n <= hi) || k0 + n <= s1);
+                if (__all_sync(0xffffffffu, whole)) {
+#pragma unroll
+                    for (int c = 0; c < SF_KT; c += 32) chunk_max(c);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < SF_KT; c += 32)
+                        if (c < n) {
+                            const int k = k0 + c;
                             const uint32_t vis = (bit_range(lo - k, hi - k) | bit_range(0, s1 - k)) & bit_range(0, n - c);
+                            if (__any_sync(0xffffffffu, vis != 0xffffffffu)) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((vis >> e) & 1u)) s[c + e] = __float_as_uint(-INFINITY);
+                                for (int e = 0; e < 32; ++e)
+                                    if (!((vis >> e) & 1u)) s[c + e] = __float_as_uint(-INFINITY);
+                            }
+                            chunk_max(c);
                         }
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            mx[(e >> 1) & 3] = fmaxf(fmaxf(mx[(e >> 1) & 3], __uint_as_float(s[c + e])),
-                                                     __uint_as_float(s[c + e + 1]));
-                    }
                 }
                 const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
                 const bool raise = mt > m + (m == -INFINITY ? 0.f : SF_RAISE);
@@ -560,68 +628,79 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
             kt0 += x.nt;
             // ------------------------------------------------------ epilogue
             if (nqi == 0) continue;
-            const long long row0 = (p.cu_q ? 0 : (long long)x.b * p.Tq) + x.s.q0 + x.t0 + i * tl.TPT;
+            // rows of the output relative to the tile's first; -1: nobody's
+            const int row_at = row_ok ? tt * p.Hq + hh : -1;
+            const long long row0 = (long long)(x.row + i * tl.TPT) * p.Hq + (x.heads & 0xfffff);
+            T *out0 = (T *)p.out + row0 * D;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            if (row_ok) p.lse[row0 + row_at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             if (!first) {
                 if (!wait_warp(o_full + i, opar, abort_flag)) { ok = false; break; }
                 opar ^= 1;
                 tc::fence_after_sync();
             }
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const bool patch = *dirty != 0;           // set once, for every later item of this CTA
+            const bool patch = *dirty != 0 && row_ok;  // set once, for every later item of this CTA
+            const uint64_t inv2 = f2_pack(inv, inv);
             // 64 columns at a time through the warp's own shared memory, so that whole lines are written
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 64) {
+                uint32_t o[64];
+                if (first) {                          // no key tile: O holds nothing of this item
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    uint32_t o[32];
-                    if (first) {                      // no key tile: O holds nothing of this item
+                    for (int e = 0; e < 64; ++e) o[e] = 0u;
+                } else {
+                    tmem_ld32(tO + c0, *reinterpret_cast<uint32_t(*)[32]>(o));
+                    tmem_ld32(tO + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
+                    tc::tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0u;
-                    } else {
-                        tmem_ld32(tO + c0 + c, o);
-                        tc::tmem_ld_wait();
+                    for (int e = 0; e < 64; e += 2) {
+                        float a, b;
+                        f2_unpack(f2_mul(f2_pack(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), inv2), a, b);
+                        o[e] = __float_as_uint(a);
+                        o[e + 1] = __float_as_uint(b);
                     }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
-                    if (patch && row_ok) {
-                        const T *vb = (const T *)p.v + (p.cu_q ? 0 : x.b) * p.v_s[0] + x.s.k0 * p.v_s[1] +
-                                      x.hk * p.v_s[2] + c0 + c;
+                }
+                if (__any_sync(0xffffffffu, patch)) {
+                    if (patch) {
+                        const long long qr = x.row;
+                        const int b = p.cu_q ? sink_find(p.cu_q, p.B, qr) : (int)(qr / p.Tq);
+                        const SinkSeq sq = sink_seq(p, max(b, 0));
+                        const T *vb = (const T *)p.v + (p.cu_q ? 0 : b) * p.v_s[0] + sq.k0 * p.v_s[1] +
+                                      (x.heads & 0xfffff) / p.G * p.v_s[2] + c0;
 #pragma unroll 1
                         for (int k = x.band_lo; k < x.band_hi; ++k) {
                             if (k == x.clean_lo && k < x.clean_hi) k = x.clean_hi;
                             if (k >= x.band_hi) break;
                             if (!(k < s1 || (k >= lo && k < hi))) continue;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
+                            for (int e = 0; e < 64; ++e) {
                                 const float v = to_f(vb[k * p.v_s[1] + e]);
                                 if (!isfinite(v)) o[e] = __float_as_uint(__uint_as_float(o[e]) + v);
                             }
                         }
                     }
+                    __syncwarp();
+                }
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        uint32_t w[4];
+                for (int u = 0; u < 8; ++u) {
+                    uint32_t w[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack2<T>(__uint_as_float(o[8 * u + 2 * e]), __uint_as_float(o[8 * u + 2 * e + 1]));
-                        *reinterpret_cast<uint4 *>(stage + lane * 128 + (((c / 8 + u) ^ (lane & 7)) * 16)) =
-                            make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = pack2<T>(__uint_as_float(o[8 * u + 2 * e]), __uint_as_float(o[8 * u + 2 * e + 1]));
+                    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((u ^ (lane & 7)) * 16)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 __syncwarp();
                 // 8 lanes per row, 4 rows at a time
-                const uint32_t good = __ballot_sync(0xffffffffu, row_ok);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int rr = k * 4 + lane / 8, u = lane % 8, ro = (warp & 3) * 32 + rr;
-                    const int rt = ro / tl.HB, rh = ro - rt * tl.HB;
+                    const int rr = k * 4 + lane / 8, u = lane % 8;
+                    const int to = __shfl_sync(0xffffffffu, row_at, rr);
                     const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((u ^ (rr & 7)) * 16));
-                    if ((good >> rr) & 1)
-                        *reinterpret_cast<uint4 *>((T *)p.out + ((row0 + rt) * p.Hq + x.h0 + rh) * D + c0 + u * 8) = v;
+                    if (to >= 0) *reinterpret_cast<uint4 *>(out0 + (long long)to * D + c0 + u * 8) = v;
                 }
                 __syncwarp();
             }
-            if (row_ok) p.lse[(row0 + tt) * p.Hq + x.h0 + hh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             tc::fence_before_sync();
         }
         if (!ok) fail();
