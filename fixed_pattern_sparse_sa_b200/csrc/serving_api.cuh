@@ -7,6 +7,7 @@
 #include "paged_attn.cuh"
 #include "paged_books.cuh"
 #include "sink_attn.cuh"
+#include "sink_bwd_tc.cuh"
 #include "sink_fwd_tc.cuh"
 
 // ---------------------------------------------------- sink-window attention --
@@ -33,7 +34,7 @@ static int sink_check(const char *what, const sa_sink_shape *s, const void *q, c
     // so are the work items: at most one per query, KV head and 128 heads of its group, and one more per sequence
     // (a step beyond the last may be formed)
     if (((cu_q ? 1ll : s->B) * s->Tq + s->B) * s->Hkv * ((s->Hq / s->Hkv + 127) / 128) >= INT_MAX / 2 ||
-        (long long)s->Hq >= (1 << 20))
+        s->Hq >= (1 << 20) || (bwd && (cu_q ? 1ll : s->B) * s->L * s->Hkv >= INT_MAX / 2))
         return fail(SA_ERR_UNSUPPORTED, "%s: too many rows", what);
     if ((cu_q == nullptr) != (cu_k == nullptr)) return fail(SA_ERR_INVALID_ARG, "%s: cu_q and cu_k go together", what);
     const bool no_q = s->Tq == 0, no_k = s->L == 0;       // an empty tensor may have a null pointer
@@ -64,13 +65,14 @@ static SinkParams sink_params(const sa_sink_shape *s, const void *q, const void 
     }
     p.cu_q = cu_q; p.cu_k = cu_k;
     p.B = s->B; p.Hq = s->Hq; p.Hkv = s->Hkv; p.G = s->Hq / s->Hkv;
-    p.window = s->window; p.sinks = s->sinks;
+    // a window past the last position and sinks past the last key say no more than these do
+    const int64_t last = cu_q ? s->L : s->q_pos0 + s->Tq;
+    p.window = (int)std::min<int64_t>(s->window, std::max<int64_t>(last, 1));
+    p.sinks = (int)std::min<int64_t>(s->sinks, s->L);
     p.Tq = s->Tq; p.L = s->L; p.q_pos0 = s->q_pos0; p.max_q = s->max_q; p.max_k = s->max_k;
     p.scale = s->scale; p.scale_log2 = s->scale * kLog2e;
     return p;
 }
-
-static unsigned sink_row_blocks(long long rows) { return (unsigned)std::min<long long>((rows + 3) / 4, 1 << 30); }
 
 // 4-D map over [batch, token, head, d] rows with the given strides (elements);
 // box = 64 columns (128 bytes) x box_heads x box_tokens, 128-byte swizzle.  A
@@ -96,12 +98,12 @@ static int rows_tensor_map(CUtensorMap *m, const void *base, int d, long long he
     return SA_OK;
 }
 
-static SinkTiles sink_tiles(const SinkParams &p) {
+static SinkTiles sink_tiles(const SinkParams &p, int row_tiles) {
     SinkTiles t{};
     t.HB = std::min(p.G, 128);
     t.HC = (p.G + 127) / 128;
     t.TPT = 128 / t.HB;
-    const long long TI = 2 * t.TPT;
+    const long long TI = (long long)row_tiles * t.TPT;
     t.per_seq = (int)((p.Tq + TI - 1) / TI);
     t.items = (int)((p.cu_q ? p.Tq / TI + p.B : (long long)p.B * t.per_seq) * p.Hkv * t.HC);
     return t;
@@ -109,7 +111,7 @@ static SinkTiles sink_tiles(const SinkParams &p) {
 
 template <typename T, int D>
 static int sink_fwd_launch(const SinkParams &p, cudaStream_t st) {
-    const SinkTiles t = sink_tiles(p);
+    const SinkTiles t = sink_tiles(p, 2);
     const long long nb = p.cu_q ? 1 : p.B;
     CUtensorMap qm, km, vm;
     // without keys nothing is loaded; the maps only have to be valid
@@ -143,25 +145,94 @@ extern "C" int sa_sink_attn_fwd(const sa_sink_shape *shape, const void *q, const
     return shape->d == 64 ? sink_fwd_launch<__half, 64>(p, st) : sink_fwd_launch<__half, 128>(p, st);
 }
 
+// Key-major items of the backward and how the sinks' are cut: pieces of a
+// quarter of a band item, so that they fill the last wave, but of 32 units at
+// least, 64 pieces at most, and no more than four waves of them in all.
+static SinkKvTiles sink_kv_tiles(const SinkParams &p) {
+    SinkKvTiles t{};
+    t.HB = std::min(p.G, 64);
+    t.HC = (p.G + 63) / 64;
+    t.TPT = 64 / t.HB;
+    const long long nq = p.cu_q ? (p.max_q ? std::min(p.max_q, p.Tq) : p.Tq) : p.Tq;
+    const long long nk = p.cu_q ? (p.max_k ? std::min(p.max_k, p.L) : p.L) : p.L;
+    const bool apart = p.cu_q ? nk > p.window : p.q_pos0 + p.Tq > p.window;
+    const long long se = apart ? std::min<long long>(p.sinks, nk) : 0;
+    t.per_seq = (int)((p.L - se + 127) / 128);                     // dense: every sequence's
+    t.band = (int)(p.cu_q ? p.L / 128 + p.B : (long long)p.B * t.per_seq);
+    t.n_kt = (int)((se + 127) / 128);
+    t.n_split = 1;
+    t.tps = (int)std::max<long long>(nq, 1);
+    if (t.n_kt && nq) {
+        const long long want = std::max({(32ll * t.TPT + t.HC - 1) / t.HC, (p.window + 131ll) / 4, (nq + 63) / 64});
+        const long long most = std::max<long long>(1, 4ll * 148 / ((long long)p.B * p.Hkv * t.n_kt));
+        t.n_split = (int)std::min(most, (nq + want - 1) / want);
+        t.tps = (int)((nq + t.n_split - 1) / t.n_split);
+    }
+    t.items = (int)((t.band + (long long)p.B * t.n_kt * t.n_split) * p.Hkv);
+    return t;
+}
+struct SinkBwdLayout { size_t counter, part, total; };
+static SinkBwdLayout sink_bwd_layout(const SinkParams &p, int d) {
+    const SinkKvTiles t = sink_kv_tiles(p);
+    SinkBwdLayout l{};
+    l.counter = round_up((size_t)(p.cu_q ? 1 : p.B) * p.Tq * p.Hq * 8, 256);
+    l.part = l.counter + 256;
+    l.total = l.part + (t.n_split > 1 ? (size_t)p.B * p.Hkv * t.n_split * p.sinks * 2 * d * 4 : 0);
+    return l;
+}
+
 extern "C" size_t sa_sink_attn_bwd_workspace_size(const sa_sink_shape *s, int packed) {
-    if (!s || s->B <= 0 || s->Tq < 0 || s->Hq <= 0) return 0;
-    return round_up((size_t)(packed ? 1 : s->B) * s->Tq * s->Hq * 8, 256);
+    if (!s || s->B <= 0 || s->Tq < 0 || s->L < 0 || s->Hq <= 0 || s->Hkv <= 0 || s->Hq % s->Hkv || s->window < 1 ||
+        s->sinks < 0)
+        return 0;
+    const int32_t *cu = packed ? reinterpret_cast<const int32_t *>(s) : nullptr;       // only whether it is there counts
+    return sink_bwd_layout(sink_params(s, nullptr, nullptr, nullptr, cu, cu), s->d).total;
 }
 
 template <int D>
-static int sink_bwd_launch(const SinkParams &p, cudaStream_t st) {
+static int sink_bwd_launch(const SinkParams &p, void *ws, cudaStream_t st) {
     using T = __nv_bfloat16;
     const long long nb = p.cu_q ? 1 : p.B;
-    if (p.Tq > 0) {
-        const unsigned g = sink_row_blocks(nb * p.Tq * p.Hq);
-        launch_k("sink_bwd_prep_kernel", sink_bwd_prep_kernel<T, D>, g, 128, 0, st, p);
-        SA_CHECK_LAUNCH("sink_bwd_prep_kernel");
-        launch_k("sink_dq_rows_kernel", sink_dq_rows_kernel<T, D>, g, 128, 0, st, p);
-        SA_CHECK_LAUNCH("sink_dq_rows_kernel");
-    }
+    const SinkBwdLayout lay = sink_bwd_layout(p, D);
+    SinkKvTiles kt = sink_kv_tiles(p);
+    kt.counter = reinterpret_cast<int *>(static_cast<char *>(ws) + lay.counter);
+    kt.part = reinterpret_cast<float *>(static_cast<char *>(ws) + lay.part);
+    const long long rows = nb * p.Tq * p.Hq;
+    launch_k("sink_bwd_prep_kernel", sink_bwd_prep_kernel<T, D>,
+             (unsigned)std::min<long long>(std::max<long long>((rows + 3) / 4, 1), 1 << 20), 128, 0, st, p, kt.counter);
+    SA_CHECK_LAUNCH("sink_bwd_prep_kernel");
+    // an empty side is never loaded: its maps only have to be valid
+    const void *any = p.Tq ? p.q : p.k, *q = any, *g = p.Tq ? p.dout : any, *k = p.L ? p.k : any, *v = p.L ? p.v : any;
+    const long long Tq = std::max(p.Tq, 1ll), L = std::max(p.L, 1ll);
+    CUtensorMap km, vm, qm, gm;
+    int rc = rows_tensor_map<T>(&km, k, D, p.Hkv, L, nb, p.k_s, 1, 128);
+    if (!rc) rc = rows_tensor_map<T>(&vm, v, D, p.Hkv, L, nb, p.v_s, 1, 128);
+    if (rc) return rc;
     if (p.L > 0) {
-        launch_k("sink_dkv_rows_kernel", sink_dkv_rows_kernel<T, D>, sink_row_blocks(nb * p.L * p.Hkv), 128, 0, st, p);
-        SA_CHECK_LAUNCH("sink_dkv_rows_kernel");
+        rc = rows_tensor_map<T>(&qm, q, D, p.Hq, Tq, nb, p.q_s, kt.HB, kt.TPT);
+        if (!rc) rc = rows_tensor_map<T>(&gm, g, D, p.Hq, Tq, nb, p.do_s, kt.HB, kt.TPT);
+        if (!rc) rc = set_smem(sink_dkv_tc_kernel<D>, SkSmem<D>::ALLOC);
+        if (rc) return rc;
+        const unsigned grid = (unsigned)std::min(std::max(kt.items, 1), sm_count());
+        launch_k("sink_dkv_tc_kernel", sink_dkv_tc_kernel<D>, grid, SB_THREADS, SkSmem<D>::ALLOC, st, qm, gm, km, vm, p,
+                 kt);
+        SA_CHECK_LAUNCH("sink_dkv_tc_kernel");
+        if (kt.n_split > 1) {
+            const long long jr = (long long)p.B * p.Hkv * p.sinks;
+            launch_k("sink_dkv_join_kernel", sink_dkv_join_kernel<D>, (unsigned)std::min<long long>((jr + 3) / 4, 1 << 20),
+                     128, 0, st, p, kt);
+            SA_CHECK_LAUNCH("sink_dkv_join_kernel");
+        }
+    }
+    if (p.Tq > 0) {
+        const SinkTiles t = sink_tiles(p, 1);
+        rc = rows_tensor_map<T>(&qm, q, D, p.Hq, Tq, nb, p.q_s, t.HB, t.TPT);
+        if (!rc) rc = rows_tensor_map<T>(&gm, g, D, p.Hq, Tq, nb, p.do_s, t.HB, t.TPT);
+        if (!rc) rc = set_smem(sink_dq_tc_kernel<D>, SqSmem<D>::ALLOC);
+        if (rc) return rc;
+        const unsigned grid = (unsigned)std::min(t.items, sm_count());
+        launch_k("sink_dq_tc_kernel", sink_dq_tc_kernel<D>, grid, SB_THREADS, SqSmem<D>::ALLOC, st, qm, gm, km, vm, p, t);
+        SA_CHECK_LAUNCH("sink_dq_tc_kernel");
     }
     return SA_OK;
 }
@@ -190,8 +261,9 @@ extern "C" int sa_sink_attn_bwd(const sa_sink_shape *shape, const void *q, const
     if (rc) return rc;
     p.o = out; p.lse_in = lse; p.dout = dout;
     p.dq = dq; p.dk = dk; p.dv = dv; p.stat = static_cast<float2 *>(workspace);
+    if (shape->Tq == 0 && shape->L == 0) return SA_OK;
     cudaStream_t st = as_stream(stream);
-    return shape->d == 64 ? sink_bwd_launch<64>(p, st) : sink_bwd_launch<128>(p, st);
+    return shape->d == 64 ? sink_bwd_launch<64>(p, workspace, st) : sink_bwd_launch<128>(p, workspace, st);
 }
 
 // ------------------------------------------------- paged decode attention --

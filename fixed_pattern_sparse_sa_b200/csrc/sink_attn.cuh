@@ -101,11 +101,13 @@ __device__ __forceinline__ unsigned pack2(float lo, float hi) {
     }
 }
 
-// Per row and head: the lse in base 2 and D = dout . out.
+// Per row and head: the lse in base 2 and D = dout . out.  Also resets the
+// key-major pass's item counter.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) sink_bwd_prep_kernel(const SinkParams p) {
+__global__ void __launch_bounds__(128) sink_bwd_prep_kernel(const SinkParams p, int *counter) {
     grid_dependency_sync();
     sink_report(p);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
     const long long rows = (p.cu_q ? 1 : p.B) * p.Tq * p.Hq;
@@ -119,89 +121,6 @@ __global__ void __launch_bounds__(128) sink_bwd_prep_kernel(const SinkParams p) 
         x = warp_sum(x);
         if (lane == 0)
             p.stat[w] = make_float2(p.lse_in[b * p.lse_s[0] + t * p.lse_s[1] + h * p.lse_s[2]] * kLog2e, x);
-    }
-}
-
-// dq: one warp per query row and head.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) sink_dq_rows_kernel(const SinkParams p) {
-    grid_dependency_sync();
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long rows = (p.cu_q ? 1 : p.B) * p.Tq * p.Hq;
-    for (long long w = blockIdx.x * 4ll + (threadIdx.x >> 5); w < rows; w += gridDim.x * 4ll) {
-        const int h = (int)(w % p.Hq), g = h / p.G;
-        const long long r = w / p.Hq;
-        const int b = p.cu_q ? sink_find(p.cu_q, p.B, r) : (int)(r / p.Tq);
-        if (b < 0) continue;
-        const SinkSeq s = sink_seq(p, b);
-        const long long t = p.cu_q ? r - s.q0 : r % p.Tq;
-        if (t < 0 || t >= s.nq) continue;
-        const long long bq = p.cu_q ? 0 : b;
-        const T *q = (const T *)p.q + bq * p.q_s[0] + (s.q0 + t) * p.q_s[1] + h * p.q_s[2] + lane * E;
-        const T *dp = (const T *)p.dout + bq * p.do_s[0] + (s.q0 + t) * p.do_s[1] + h * p.do_s[2] + lane * E;
-        const T *kb = (const T *)p.k + bq * p.k_s[0] + s.k0 * p.k_s[1] + g * p.k_s[2] + lane * E;
-        const T *vb = (const T *)p.v + bq * p.v_s[0] + s.k0 * p.v_s[1] + g * p.v_s[2] + lane * E;
-        float qf[E], gf[E], dq[E] = {};
-        for (int e = 0; e < E; ++e) { qf[e] = to_f(q[e]); gf[e] = to_f(dp[e]); }
-        const float l2 = p.stat[w].x, Dr = p.stat[w].y;
-        int s1, lo, hi;
-        sink_visible(p, s.nk, s.pos0 + t, s1, lo, hi);
-        for (int j = s1 > 0 ? 0 : lo; j < hi; j = j + 1 == s1 ? lo : j + 1) {
-            float z = 0.f, dP = 0.f;
-            for (int e = 0; e < E; ++e) {
-                z += qf[e] * to_f(kb[j * p.k_s[1] + e]);
-                dP += gf[e] * to_f(vb[j * p.v_s[1] + e]);
-            }
-            const float dS = exp2f(warp_sum(z) * p.scale_log2 - l2) * (warp_sum(dP) - Dr);
-            for (int e = 0; e < E; ++e) dq[e] += dS * to_f(kb[j * p.k_s[1] + e]);
-        }
-        T *out = (T *)p.dq + w * D + lane * E;
-        for (int e = 0; e < E; ++e) out[e] = from_f<T>(dq[e] * p.scale);
-    }
-}
-
-// dk, dv: one warp per key row and KV head, over the queries that see it.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) sink_dkv_rows_kernel(const SinkParams p) {
-    grid_dependency_sync();
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long rows = (p.cu_q ? 1 : p.B) * p.L * p.Hkv;
-    for (long long w = blockIdx.x * 4ll + (threadIdx.x >> 5); w < rows; w += gridDim.x * 4ll) {
-        const int g = (int)(w % p.Hkv);
-        const long long r = w / p.Hkv;
-        const int b = p.cu_q ? sink_find(p.cu_k, p.B, r) : (int)(r / p.L);
-        if (b < 0) continue;
-        const SinkSeq s = sink_seq(p, b);
-        const long long j = p.cu_q ? r - s.k0 : r % p.L;
-        if (j < 0 || j >= s.nk) continue;
-        const long long bq = p.cu_q ? 0 : b;
-        const T *k = (const T *)p.k + bq * p.k_s[0] + (s.k0 + j) * p.k_s[1] + g * p.k_s[2] + lane * E;
-        const T *v = (const T *)p.v + bq * p.v_s[0] + (s.k0 + j) * p.v_s[1] + g * p.v_s[2] + lane * E;
-        float kf[E], vf[E], dk[E] = {}, dv[E] = {};
-        for (int e = 0; e < E; ++e) { kf[e] = to_f(k[e]); vf[e] = to_f(v[e]); }
-        // queries with j <= p, and p - j < window unless j is a sink
-        const long long t0 = j > s.pos0 ? j - s.pos0 : 0;
-        const long long end = j < p.sinks ? s.nq : j + p.window - s.pos0;
-        const long long t1 = end < s.nq ? end : s.nq;
-        for (long long t = t0; t < t1; ++t)
-            for (int h = g * p.G; h < (g + 1) * p.G; ++h) {
-                const T *q = (const T *)p.q + bq * p.q_s[0] + (s.q0 + t) * p.q_s[1] + h * p.q_s[2] + lane * E;
-                const T *dp = (const T *)p.dout + bq * p.do_s[0] + (s.q0 + t) * p.do_s[1] + h * p.do_s[2] + lane * E;
-                const long long row = (p.cu_q ? s.q0 + t : b * p.Tq + t) * p.Hq + h;
-                float qf[E], gf[E], z = 0.f, dP = 0.f;
-                for (int e = 0; e < E; ++e) {
-                    qf[e] = to_f(q[e]); gf[e] = to_f(dp[e]);
-                    z += qf[e] * kf[e];
-                    dP += gf[e] * vf[e];
-                }
-                const float P = exp2f(warp_sum(z) * p.scale_log2 - p.stat[row].x);
-                const float dS = P * (warp_sum(dP) - p.stat[row].y);
-                for (int e = 0; e < E; ++e) { dk[e] += dS * qf[e]; dv[e] += P * gf[e]; }
-            }
-        T *dko = (T *)p.dk + w * D + lane * E, *dvo = (T *)p.dv + w * D + lane * E;
-        for (int e = 0; e < E; ++e) { dko[e] = from_f<T>(dk[e] * p.scale); dvo[e] = from_f<T>(dv[e]); }
     }
 }
 

@@ -62,7 +62,7 @@ struct SfSmem {
 
 struct SinkTiles {
     int HB, HC, TPT;         // heads per row tile, head chunks per group, queries per row tile
-    int per_seq;             // dense: query blocks of 2 * TPT per sequence
+    int per_seq;             // dense: query blocks of TPT * (row tiles per item) per sequence
     int items;               // query blocks (packed: an upper bound) * Hkv * HC
 };
 
@@ -88,10 +88,25 @@ struct SinkItem {
         return (i ? nq_i[1] : nq_i[0]) > 0 && (j < n_sink || (j >= (i ? ja[1] : ja[0]) && j < (i ? jb[1] : jb[0])));
     }
 };
+// Block blk of a packed batch in blocks of TI rows: its sequence and the
+// block's number there.  Sequence b starts at block cu[b] / TI + b, so there
+// is room for every sequence's last, partial block; blocks past it are empty.
+__device__ __forceinline__ void sink_slot(const int32_t *cu, int B, int rows, unsigned TI, int blk, int &b, int &local) {
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+        const int m = (lo + hi) / 2;
+        const unsigned c = (unsigned)min(max(__ldg(cu + m), 0), rows);
+        if ((long long)(c / TI) + m <= blk) lo = m; else hi = m;
+    }
+    b = lo;
+    local = blk - (int)((unsigned)min(max(__ldg(cu + lo), 0), rows) / TI + lo);
+}
+// Work item `it` of NT row tiles; false: it lies past its sequence.
+template <int NT>
 __device__ __forceinline__ bool sink_item(const SinkParams &p, const SinkTiles &tl, int it, SinkItem &x) {
     const int H2 = p.Hkv * tl.HC, blk = it / H2, hh = it - blk * H2;
     const int hc = tl.HC == 1 ? 0 : hh % tl.HC;
-    const unsigned TI = 2 * tl.TPT;
+    const unsigned TI = NT * tl.TPT;
     x.hk = tl.HC == 1 ? hh : hh / tl.HC;
     x.h0 = x.hk * p.G + hc * tl.HB;
     x.nh = min(tl.HB, p.G - hc * tl.HB);
@@ -100,15 +115,7 @@ __device__ __forceinline__ bool sink_item(const SinkParams &p, const SinkTiles &
         x.b = blk / tl.per_seq;
         local = blk - x.b * tl.per_seq;
     } else {
-        // sequence b starts at block cu[b] / TI + b: the last start at or before blk
-        int lo = 0, hi = p.B;
-        while (hi - lo > 1) {
-            const int m = (lo + hi) / 2;
-            const unsigned c = (unsigned)min(max(__ldg(p.cu_q + m), 0), (int)p.Tq);
-            if ((long long)(c / TI) + m <= blk) lo = m; else hi = m;
-        }
-        x.b = lo;
-        local = blk - (int)((unsigned)min(max(__ldg(p.cu_q + lo), 0), (int)p.Tq) / TI + lo);
+        sink_slot(p.cu_q, p.B, (int)p.Tq, TI, blk, x.b, local);
     }
     x.s = sink_seq(p, x.b);
     if (local < 0 || (long long)local * TI >= x.s.nq) return false;
@@ -124,7 +131,7 @@ __device__ __forceinline__ bool sink_item(const SinkParams &p, const SinkTiles &
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int ta = x.t0 + i * tl.TPT;
-        x.nq_i[i] = max(0, min(tl.TPT, x.s.nq - ta));
+        x.nq_i[i] = i < NT ? max(0, min(tl.TPT, x.s.nq - ta)) : 0;
         lo_min[i] = hi_max[i] = s1_max[i] = 0;
         if (x.nq_i[i] == 0) continue;
         sink_visible(p, x.s.nk, x.s.pos0 + ta, s1, lo, hi);
@@ -399,7 +406,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
             };
             for (int it = blockIdx.x; it < tl.items && ok; it += gridDim.x) {
                 SinkItem x;
-                if (!sink_item(p, tl, it, x)) continue;
+                if (!sink_item<2>(p, tl, it, x)) continue;
                 ok = hand_over(SfItem{x.nt, {x.nq_i[0], x.nq_i[1]}, (int)x.s.pos0 + x.t0, x.band_lo, x.band_hi, x.s_end,
                                       x.n_sink, {x.ja[0], x.ja[1]}, {x.jb[0], x.jb[1]}, x.clean_lo, x.clean_hi,
                                       x.h0 | x.nh << 20,
