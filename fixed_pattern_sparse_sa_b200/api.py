@@ -673,18 +673,19 @@ def sink_attn_bwd(q, k, v, out, lse, dout, window: int, sinks: int = 0, cu_q=Non
                   q_pos0: Optional[int] = None, dq=None, dk=None, dv=None):
     """Backward of sink_attn_fwd (sa_sink_attn_bwd), bf16.
 
-    out and lse are the forward's; the other arguments as there.  Returns
-    (dq, dk, dv), bf16, shaped like q, k and v; rows outside every packed
+    out and lse are the forward's (out may be None: only lse is read); the
+    other arguments as there.  Returns (dq, dk, dv), bf16, shaped like q, k and v; rows outside every packed
     sequence are left as they were.
     """
     lib = _lib.load()
     s, dev, packed = _sink_shape("sink_attn_bwd", q, k, v, window, sinks, cu_q, cu_k, max_q, max_k, scale, q_pos0,
                                  (torch.bfloat16,))
     _need_rows(dout, "dout", torch.bfloat16, dev, q.shape)
-    _need_rows(out, "out", torch.bfloat16, dev, q.shape)
+    if out is not None:
+        _need_rows(out, "out", torch.bfloat16, dev, q.shape)
     if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or lse.device != dev or lse.shape != q.shape[:-1]:
         raise ValueError("sink_attn_bwd: lse must be the forward's, fp32 and shaped like q without d")
-    for dst, t in ((s.out_stride, out), (s.dout_stride, dout), (s.lse_stride, lse)):
+    for dst, t in ((s.dout_stride, dout), (s.lse_stride, lse)):
         _set_strides(dst, t, packed)
     dq = _need_out(dq, "dq", torch.bfloat16, dev, q.shape)
     dk = _need_out(dk, "dk", torch.bfloat16, dev, k.shape)
@@ -692,7 +693,7 @@ def sink_attn_bwd(q, k, v, out, lse, dout, window: int, sinks: int = 0, cu_q=Non
     with _on_device(dev):
         nbytes = lib.sa_sink_attn_bwd_workspace_size(ctypes.byref(s), int(packed))
         ws = _workspace(nbytes, dev)
-        check(lib.sa_sink_attn_bwd(ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+        check(lib.sa_sink_attn_bwd(ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(out),
                                    lse.data_ptr(), dout.data_ptr(), _ptr(cu_q), _ptr(cu_k), dq.data_ptr(),
                                    dk.data_ptr(), dv.data_ptr(), _ptr(ws), nbytes, _stream(dev)), "sa_sink_attn_bwd")
     return dq, dk, dv

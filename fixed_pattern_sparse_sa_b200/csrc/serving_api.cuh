@@ -61,7 +61,7 @@ static SinkParams sink_params(const sa_sink_shape *s, const void *q, const void 
     p.q = q; p.k = k; p.v = v;
     for (int i = 0; i < 3; ++i) {
         p.q_s[i] = s->q_stride[i]; p.k_s[i] = s->k_stride[i]; p.v_s[i] = s->v_stride[i];
-        p.o_s[i] = s->out_stride[i]; p.do_s[i] = s->dout_stride[i]; p.lse_s[i] = s->lse_stride[i];
+        p.do_s[i] = s->dout_stride[i]; p.lse_s[i] = s->lse_stride[i];
     }
     p.cu_q = cu_q; p.cu_k = cu_k;
     p.B = s->B; p.Hq = s->Hq; p.Hkv = s->Hkv; p.G = s->Hq / s->Hkv;
@@ -197,10 +197,6 @@ static int sink_bwd_launch(const SinkParams &p, void *ws, cudaStream_t st) {
     SinkKvTiles kt = sink_kv_tiles(p);
     kt.counter = reinterpret_cast<int *>(static_cast<char *>(ws) + lay.counter);
     kt.part = reinterpret_cast<float *>(static_cast<char *>(ws) + lay.part);
-    const long long rows = nb * p.Tq * p.Hq;
-    launch_k("sink_bwd_prep_kernel", sink_bwd_prep_kernel<T, D>,
-             (unsigned)std::min<long long>(std::max<long long>((rows + 3) / 4, 1), 1 << 20), 128, 0, st, p, kt.counter);
-    SA_CHECK_LAUNCH("sink_bwd_prep_kernel");
     // an empty side is never loaded: its maps only have to be valid
     const void *any = p.Tq ? p.q : p.k, *q = any, *g = p.Tq ? p.dout : any, *k = p.L ? p.k : any, *v = p.L ? p.v : any;
     const long long Tq = std::max(p.Tq, 1ll), L = std::max(p.L, 1ll);
@@ -208,6 +204,21 @@ static int sink_bwd_launch(const SinkParams &p, void *ws, cudaStream_t st) {
     int rc = rows_tensor_map<T>(&km, k, D, p.Hkv, L, nb, p.k_s, 1, 128);
     if (!rc) rc = rows_tensor_map<T>(&vm, v, D, p.Hkv, L, nb, p.v_s, 1, 128);
     if (rc) return rc;
+    // first: it also writes the rows' lse and D for the key-major pass, and resets its counter
+    if (p.Tq > 0) {
+        const SinkTiles t = sink_tiles(p, 1);
+        rc = rows_tensor_map<T>(&qm, q, D, p.Hq, Tq, nb, p.q_s, t.HB, t.TPT);
+        if (!rc) rc = rows_tensor_map<T>(&gm, g, D, p.Hq, Tq, nb, p.do_s, t.HB, t.TPT);
+        if (!rc) rc = set_smem(sink_dq_tc_kernel<D>, SqSmem<D>::ALLOC);
+        if (rc) return rc;
+        const unsigned grid = (unsigned)std::min(t.items, sm_count());
+        launch_k("sink_dq_tc_kernel", sink_dq_tc_kernel<D>, grid, SB_THREADS, SqSmem<D>::ALLOC, st, qm, gm, km, vm, p, t,
+                 kt.counter);
+        SA_CHECK_LAUNCH("sink_dq_tc_kernel");
+    } else {
+        const cudaError_t e = cudaMemsetAsync(kt.counter, 0, sizeof(int), st);
+        if (e != cudaSuccess) return fail(SA_ERR_CUDA, "sink_attn_bwd memset: %s", cudaGetErrorString(e));
+    }
     if (p.L > 0) {
         rc = rows_tensor_map<T>(&qm, q, D, p.Hq, Tq, nb, p.q_s, kt.HB, kt.TPT);
         if (!rc) rc = rows_tensor_map<T>(&gm, g, D, p.Hq, Tq, nb, p.do_s, kt.HB, kt.TPT);
@@ -224,16 +235,6 @@ static int sink_bwd_launch(const SinkParams &p, void *ws, cudaStream_t st) {
             SA_CHECK_LAUNCH("sink_dkv_join_kernel");
         }
     }
-    if (p.Tq > 0) {
-        const SinkTiles t = sink_tiles(p, 1);
-        rc = rows_tensor_map<T>(&qm, q, D, p.Hq, Tq, nb, p.q_s, t.HB, t.TPT);
-        if (!rc) rc = rows_tensor_map<T>(&gm, g, D, p.Hq, Tq, nb, p.do_s, t.HB, t.TPT);
-        if (!rc) rc = set_smem(sink_dq_tc_kernel<D>, SqSmem<D>::ALLOC);
-        if (rc) return rc;
-        const unsigned grid = (unsigned)std::min(t.items, sm_count());
-        launch_k("sink_dq_tc_kernel", sink_dq_tc_kernel<D>, grid, SB_THREADS, SqSmem<D>::ALLOC, st, qm, gm, km, vm, p, t);
-        SA_CHECK_LAUNCH("sink_dq_tc_kernel");
-    }
     return SA_OK;
 }
 
@@ -244,11 +245,10 @@ extern "C" int sa_sink_attn_bwd(const sa_sink_shape *shape, const void *q, const
     SA_TRACE("sa_sink_attn_bwd");
     int rc = sink_check("sink_attn_bwd", shape, q, k, v, cu_q, cu_k, true);
     if (rc) return rc;
-    if (!strides_ok(shape->out_stride, 3, 8) || !strides_ok(shape->dout_stride, 3, 8) ||
-        !strides_ok(shape->lse_stride, 3, 1))
+    if (!strides_ok(shape->dout_stride, 3, 8) || !strides_ok(shape->lse_stride, 3, 1))
         return fail(SA_ERR_INVALID_ARG, "sink_attn_bwd: strides must be multiples of 8 elements, not negative");
-    if (shape->Tq > 0 && (!out || !lse || !dout || !dq || !aligned16(out) || !aligned4(lse) || !aligned16(dout) ||
-                          !aligned16(dq)))
+    (void)out;
+    if (shape->Tq > 0 && (!lse || !dout || !dq || !aligned4(lse) || !aligned16(dout) || !aligned16(dq)))
         return fail(SA_ERR_INVALID_ARG, "sink_attn_bwd: null or misaligned pointer");
     if (shape->L > 0 && (!dk || !dv || !aligned16(dk) || !aligned16(dv)))
         return fail(SA_ERR_INVALID_ARG, "sink_attn_bwd: null or misaligned pointer");
@@ -259,7 +259,7 @@ extern "C" int sa_sink_attn_bwd(const sa_sink_shape *shape, const void *q, const
     SinkParams p = sink_params(shape, q, k, v, cu_q, cu_k);
     rc = device_error_word(&p.err);
     if (rc) return rc;
-    p.o = out; p.lse_in = lse; p.dout = dout;
+    p.lse_in = lse; p.dout = dout;
     p.dq = dq; p.dk = dk; p.dv = dv; p.stat = static_cast<float2 *>(workspace);
     if (shape->Tq == 0 && shape->L == 0) return SA_OK;
     cudaStream_t st = as_stream(stream);

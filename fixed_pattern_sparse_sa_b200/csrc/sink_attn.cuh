@@ -3,7 +3,7 @@
 //
 //   V(p) = { j <= min(p, n_k - 1) : p - j < window or j < sinks }
 //   z_j = scale q.k_j,  lse = log sum exp z,  out = sum exp(z_j - lse) v_j
-//   P = exp(z - lse), D = dout.out, dS = P (dout.v - D)
+//   P = exp(z - lse), D = sum_j P dout.v, dS = P (dout.v - D)
 //   dq = scale sum_j dS k_j,  dk_j = scale sum dS q,  dv_j = sum P dout
 #pragma once
 
@@ -14,8 +14,8 @@
 namespace sa {
 
 struct SinkParams {
-    const void *q, *k, *v, *dout, *o;
-    long long q_s[3], k_s[3], v_s[3], o_s[3], do_s[3], lse_s[3];   // batch, token, head strides (elements)
+    const void *q, *k, *v, *dout;
+    long long q_s[3], k_s[3], v_s[3], do_s[3], lse_s[3];   // batch, token, head strides (elements)
     const int32_t *cu_q, *cu_k;                  // packed: [B + 1] each; NULL: dense
     int B, Hq, Hkv, G;
     int window, sinks;
@@ -26,7 +26,7 @@ struct SinkParams {
     float *lse;                                  // the forward's result
     const float *lse_in;                         // the backward's input
     void *dq, *dk, *dv;
-    float2 *stat;                                // [rows of q, Hq] lse in base 2 and D = dout . out
+    float2 *stat;                                // [rows of q, Hq] lse in base 2 and D, from the query-major pass
     unsigned *err;
 };
 
@@ -98,29 +98,6 @@ __device__ __forceinline__ unsigned pack2(float lo, float hi) {
     } else {
         __half2 h = __floats2half2_rn(lo, hi);
         return *reinterpret_cast<unsigned *>(&h);
-    }
-}
-
-// Per row and head: the lse in base 2 and D = dout . out.  Also resets the
-// key-major pass's item counter.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) sink_bwd_prep_kernel(const SinkParams p, int *counter) {
-    grid_dependency_sync();
-    sink_report(p);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long rows = (p.cu_q ? 1 : p.B) * p.Tq * p.Hq;
-    for (long long w = blockIdx.x * 4ll + (threadIdx.x >> 5); w < rows; w += gridDim.x * 4ll) {
-        const int h = (int)(w % p.Hq);
-        const long long r = w / p.Hq, b = p.cu_q ? 0 : r / p.Tq, t = p.cu_q ? r : r % p.Tq;
-        const T *g = (const T *)p.dout + b * p.do_s[0] + t * p.do_s[1] + h * p.do_s[2] + lane * E;
-        const T *o = (const T *)p.o + b * p.o_s[0] + t * p.o_s[1] + h * p.o_s[2] + lane * E;
-        float x = 0.f;
-        for (int e = 0; e < E; ++e) x += to_f(g[e]) * to_f(o[e]);
-        x = warp_sum(x);
-        if (lane == 0)
-            p.stat[w] = make_float2(p.lse_in[b * p.lse_s[0] + t * p.lse_s[1] + h * p.lse_s[2]] * kLog2e, x);
     }
 }
 

@@ -1,8 +1,12 @@
 // sink_bwd_tc.cuh -- backward of the sink-window attention on the tcgen05
 // tensor cores.
 //
-//   P = exp(z - lse), D = dout.out, dS = P (dout.v - D)
+//   P = exp(z - lse), dP = dout.v, D = sum_j P dP, dS = P (dP - D)
 //   dq = scale sum_j dS k_j,  dk_j = scale sum dS q,  dv_j = sum P dout
+//
+// D equals dout.out, but out is stored rounded: where a row's attention lies
+// on few keys that rounding is as large as dS's own (two visible keys: dq off
+// by 2^-8.7 more than rounding it costs), so D is summed here, in fp32.
 //
 // Two passes, each with its sums in tensor memory from first to last, so
 // nothing is added up in global memory and the result does not depend on the
@@ -29,10 +33,13 @@ constexpr int SB_REGS_SCORE = 208, SB_REGS_ISSUE = 88;     // as in the forward:
 // Tensor memory holds S twice, dP once and dq: S of the next tile runs while
 // the score warps work on this one, dP of the next as soon as they have read
 // dP into registers.  dS replaces S and is the A operand of the last product.
+// The item's key tiles are walked twice: for D (S and dP only), then for dq.
 //
 // Warps: 0-7 score and epilogue (thread = row; warps 0-3 the first 64 keys of
 // a tile, 4-7 the rest), 8 TMA producer, 9 MMA issuer of S and dP and TMEM
 // owner, 10 MMA issuer of dq.
+// beside the forward's tile facts: a tile of the walk for D, the first of the walk for dq
+enum : uint32_t { TI_SUM = 512u, TI_START = 1024u };
 constexpr uint32_t DQT_S = 0, DQT_DP = 256, DQT_DQ = 384;
 
 template <int D>
@@ -47,7 +54,8 @@ struct SqSmem {
     static constexpr int N_BAR = 24;
     static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;   // tmem slot, abort flag, -, -, tile info[2]
     static constexpr int OFF_ITEM = OFF_MISC + 32;
-    static constexpr int TOTAL = OFF_ITEM + 2 * 64;
+    static constexpr int OFF_D = OFF_ITEM + 2 * 64;        // [2][128] halves of D
+    static constexpr int TOTAL = OFF_D + 1024;
     static constexpr int ALLOC = TOTAL + 1024;
     static_assert(8 * 32 * D <= 2 * TILE, "the staged rows fit the item's Q and dO");
 };
@@ -56,7 +64,7 @@ template <int D>
 __global__ void __launch_bounds__(SB_THREADS, 1)
     sink_dq_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap domap,
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                      const __grid_constant__ SinkParams p, const __grid_constant__ SinkTiles tl) {
+                      const __grid_constant__ SinkParams p, const __grid_constant__ SinkTiles tl, int *counter) {
     grid_dependency_sync();
     using T = __nv_bfloat16;
     using L = SqSmem<D>;
@@ -76,7 +84,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         tc::tmem_alloc(tmem_slot, 512);
         tc::tmem_relinquish();
     }
+    sink_report(p);
     if (tid == 0) {
+        if (blockIdx.x == 0) *counter = 0;            // the key-major pass's next item
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(q_full + i, 1); tc::mbar_init(q_empty + i, 256);
             tc::mbar_init(k_full + i, 1); tc::mbar_init(k_empty + i, 1);
@@ -132,13 +142,14 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                     load_4d(dst + L::TILE, &domap, h * 64, x.h0, (int)(x.s.q0 + x.t0), cb, q_full + qb);
                 }
                 ++qn;
-                for (int j = 0; j < x.nt && ok; ++j, ++t) {
+                for (int i = 0; i < 2 * x.nt && ok; ++i, ++t) {
+                    const bool sum = i < x.nt;
+                    const int j = sum ? i : i - x.nt, sl = t & 1;
                     int k0, n;
                     x.tile(j, k0, n);
-                    const int sl = t & 1;
                     if (!(ok = atc::wait(k_empty + sl, ((t >> 1) & 1) ^ 1, abort_flag))) break;
-                    info_s[sl] = (uint32_t)((n + 15) / 16) | (j == 0 ? TI_FIRST : 0u) | (j + 1 == x.nt ? TI_LAST : 0u) |
-                                 TI_TILE;
+                    info_s[sl] = (uint32_t)((n + 15) / 16) | (i == 0 ? TI_FIRST : 0u) | (sum ? TI_SUM : 0u) |
+                                 (i == x.nt ? TI_START : 0u) | (i + 1 == 2 * x.nt ? TI_LAST : 0u) | TI_TILE;
                     atc::expect_tx(k_full + sl, L::TILE);
                     for (int h = 0; h < HALVES; ++h)
                         load_4d(smem + L::OFF_K + sl * L::TILE + h * (128 * 128), &kmap, h * 64, x.hk,
@@ -186,7 +197,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                     if (!(ok = wait_warp(q_full + (qn & 1), (qn >> 1) & 1, abort_flag))) break;
                     ++qn;
                 }
-                // S buffer sl is free: this K tile was loaded after dq of tile t - 2 had read its dS
+                // S buffer sl is free: this K tile was loaded after tile t - 2 was done with
                 const uint64_t a = qd + (((qn - 1) & 1) * 2) * TSTEP, b = kd + sl * TSTEP;
                 const uint32_t id = tc::make_idesc(1, 1, 128, 0) | ((info & TI_STEPS) << 18);
                 tc::fence_after_sync();
@@ -228,6 +239,10 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                 if (!(info & TI_TILE)) break;
                 // the score warps write an item's first dS after they have read the dq of the item before
                 if (!(ok = wait_warp(ds_full + sl, (t >> 1) & 1, abort_flag))) break;
+                if (info & TI_SUM) {
+                    if (leader) atc::arrive(k_empty + sl);
+                    continue;
+                }
                 tc::fence_after_sync();
                 if (leader) {
                     const uint64_t b = kd + sl * (L::TILE >> 4);
@@ -236,7 +251,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                     for (int c = 0; c < 8; ++c)
                         if (c < steps)
                             tc::mma_bf16_ts(tmem + DQT_DQ, tmem + DQT_S + sl * 128 + (c / 4) * 64 + (c % 4) * 8, b + c * 128,
-                                            ID_Q, c > 0 ? 1u : (info & TI_FIRST ? 0u : 1u));
+                                            ID_Q, c > 0 ? 1u : (info & TI_START ? 0u : 1u));
                     tc::mma_commit(k_empty + sl);
                     if (info & TI_LAST) tc::mma_commit(dq_full);
                 }
@@ -278,11 +293,22 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                 hi = min(max(pos + 1, 0), x.band_hi);
                 lo = min(max(pos - p.window + 1, 0), hi);
                 s1 = min(p.sinks, lo);
-                const float2 st = __ldg(p.stat + row0 + row_at);
-                nl = -st.x;
-                Dr = st.y;
+                const int b = p.cu_q ? 0 : x.row / (int)p.Tq, tok = x.row - b * (int)p.Tq + tt;
+                nl = -kLog2e * __ldg(p.lse_in + b * p.lse_s[0] + tok * p.lse_s[1] + ((x.heads & 0xfffff) + hh) * p.lse_s[2]);
             }
-            for (int j = 0; j < x.nt; ++j, ++t) {
+            uint64_t dsum[2] = {0ull, 0ull};
+            for (int i = 0; i < 2 * x.nt; ++i, ++t) {
+                const bool sum = i < x.nt;
+                const int j = sum ? i : i - x.nt;
+                if (i == x.nt) {
+                    // D from the two halves of the row
+                    float *xd = reinterpret_cast<float *>(smem + L::OFF_D), d0, d1;
+                    f2_unpack(f2_add(dsum[0], dsum[1]), d0, d1);
+                    xd[w * 128 + r] = d0 + d1;
+                    atc::named_sync(1, 256);
+                    Dr = xd[r] + xd[128 + r];
+                    if (w == 0 && row_ok) p.stat[row0 + row_at] = make_float2(-nl, Dr);
+                }
                 const bool sink = j < x.n_sink;
                 const int k0 = sink ? j * SF_KT : x.band_lo + (j - x.n_sink) * SF_KT;
                 const int n = min(SF_KT, (sink ? x.s_end : x.band_hi) - k0), sb = t & 1;
@@ -303,7 +329,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                 tc::tmem_ld_wait();
                 tc::fence_before_sync();
                 atc::arrive(dp_free);
-                if (n & 15) {
+                if (sum) {
+                    atc::arrive(ds_full + sb);            // S has been read
+                } else if (n & 15) {
                     // rows n .. of the last 16 keys hold whatever lies behind: 0 * inf must not reach dq
                     constexpr int U = D / 8;
                     const int n16 = (n + 15) & ~15;
@@ -326,6 +354,24 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                         if (!__all_sync(0xffffffffu, whole))
                             vis = (bit_range(lo - k, hi - k) | bit_range(0, s1 - k)) & bit_range(0, n - c0 - c);
                         const bool all = __all_sync(0xffffffffu, vis == 0xffffffffu);
+                        if (sum) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                float a, b;
+                                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])), sc2, nl2),
+                                          a, b);
+                                a = ex2_fast(a);
+                                b = ex2_fast(b);
+                                float u = __uint_as_float(dp[c + e]), v = __uint_as_float(dp[c + e + 1]);
+                                if (!all) {               // both factors: dP of an unseen key may be anything
+                                    const bool v0 = (vis >> e) & 1u, v1 = (vis >> (e + 1)) & 1u;
+                                    a = v0 ? a : 0.f; u = v0 ? u : 0.f;
+                                    b = v1 ? b : 0.f; v = v1 ? v : 0.f;
+                                }
+                                dsum[(e >> 1) & 1] = f2_fma(f2_pack(a, b), f2_pack(u, v), dsum[(e >> 1) & 1]);
+                            }
+                            continue;
+                        }
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             float a, b, u, v;
@@ -344,9 +390,11 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                         atc::tmem_st16(tS + c / 2, pk);
                     }
                 }
-                atc::tmem_st_wait();
-                tc::fence_before_sync();
-                atc::arrive(ds_full + sb);
+                if (!sum) {
+                    atc::tmem_st_wait();
+                    tc::fence_before_sync();
+                    atc::arrive(ds_full + sb);
+                }
             }
             if (!ok) break;
             // ------------------------------------------------------ epilogue

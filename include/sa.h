@@ -394,8 +394,10 @@ int sa_index_shard(const int32_t *idx, int64_t n, int64_t key_lo, int64_t key_hi
  * multiple of 8 elements and not 0 over more than one step (no broadcast
  * inputs), every base 16-byte aligned.  out, dq [.., Hq, d],
  * dk, dv [.., Hkv, d] have the inputs' type, lse is fp32 [.., Hq], natural log;
- * all are written contiguous.  The backward reads the forward's out and lse
- * through strides too (lse: any).  dq, dk and dv are written, not accumulated; the result does not
+ * all are written contiguous.  The backward reads the forward's lse through
+ * any strides; out may be NULL, it is not read: D is summed as sum_j P_j
+ * (dout . v_j) in fp32, which the rounded out does not give.  dq, dk and dv are
+ * written, not accumulated; the result does not
  * depend on the order in which blocks run.  Values at keys outside V(p) do
  * not reach a forward row, infinities and NaN included; the backward wants
  * finite inputs within a sequence (what lies outside every sequence, or
@@ -412,7 +414,7 @@ typedef struct sa_sink_shape {
     int64_t q_pos0;             /* dense only */
     int64_t max_q, max_k;       /* packed only: upper bounds of the lengths, 0 = not known */
     int64_t q_stride[3], k_stride[3], v_stride[3];                  /* batch, token, head */
-    int64_t out_stride[3], dout_stride[3], lse_stride[3];           /* backward only */
+    int64_t dout_stride[3], lse_stride[3];                          /* backward only */
 } sa_sink_shape;
 
 int sa_sink_attn_fwd(const sa_sink_shape *shape, const void *q, const void *k, const void *v, const int32_t *cu_q,

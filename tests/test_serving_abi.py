@@ -25,7 +25,7 @@ def _sink(**kw):
     base = dict(dtype=0, B=2, Hq=4, Hkv=2, d=64, window=8, sinks=2, scale=0.1, Tq=16, L=16, q_pos0=0)
     for k, v in {**base, **{a: b for a, b in kw.items() if not a.endswith("stride")}}.items():
         setattr(s, k, v)
-    for name, heads in (("q_stride", 4), ("k_stride", 2), ("v_stride", 2), ("out_stride", 4), ("dout_stride", 4)):
+    for name, heads in (("q_stride", 4), ("k_stride", 2), ("v_stride", 2), ("dout_stride", 4)):
         for i, x in enumerate(kw.get(name, (16 * heads * 64, heads * 64, 64))):
             getattr(s, name)[i] = x
     return ctypes.byref(s)
