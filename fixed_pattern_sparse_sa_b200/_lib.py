@@ -83,6 +83,8 @@ def load() -> ctypes.CDLL:
     """Load libsa.so (built in-tree).  Raises if it is missing: there is no
     fallback implementation of any operation."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -134,7 +136,7 @@ def load() -> ctypes.CDLL:
             "sa_paged_attn_decode": (I, [P, P, P, P, P, P, P, P, P, SZ, P]),
             "sa_paged_books_workspace_size": (SZ, [I, I, I64]),
             "sa_paged_extend": (I, [P, P, P, I, I, I64, I, P, P, I, P, P, SZ, P]),
-            "sa_paged_write": (I, [P, P, P, P, P, P, P, P, I, I64, I, I, I64, I, I, I, I, P, P, P, P, P]),
+            "sa_paged_write": (I, [P, P, P, P, P, P, P, P, I, I64, I, I, I64, I, I, I, I, P, P]),
             "sa_paged_fork": (I, [P, P, P, I, I, I64, I, P, P, I, P, I, I64, P, P, SZ, P]),
             "sa_paged_free": (I, [P, P, P, I, I, I64, I, P, I, I, I, P]),
             "sa_paged_compact": (I, [P, P, I, I, I64, I, P, I, I64, P, P, SZ, P]),

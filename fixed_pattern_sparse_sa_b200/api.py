@@ -9,13 +9,13 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import Optional, Sequence
 
 import torch
 
 from . import _lib
-from ._lib import (SAError, check, sa_dsa_layer, sa_page_cache, sa_paged_shape, sa_pattern,
-                   sa_sink_shape)
+from ._lib import SAError, check, sa_dsa_layer, sa_pattern
 
 __all__ = ["indexer_topk", "sparse_attn_fwd", "sparse_attn_bwd", "sparse_attn_fwd_split_static", "lse_combine",
            "nsa_fwd", "sink_attn_fwd", "sink_attn_bwd", "paged_attn_decode", "paged_extend", "paged_write",
@@ -538,15 +538,23 @@ def dsa_decode_workspace_bytes(B, Tq, L, Hq, d, Hi, di, topk, window=0, n_split=
 
 
 # ------------------------------------------------- sink-window attention --
+# These entry points serve single tokens, where a call costs less on the device
+# than a careless binding on the host: the checks take a short way for tensors
+# as they should be, and the slow helpers only word the refusal.
 _ATTN_TYPES = {torch.bfloat16: _lib.SA_BF16, torch.float16: _lib.SA_FP16}
+_SINK_SHAPE = struct.Struct("=7if20q")             # sa_sink_shape
+_INT_MAX = 2 ** 31 - 1                              # a longer window sees no more
+_PAGED_SHAPE = struct.Struct("=9if9q")             # sa_paged_shape
+assert _SINK_SHAPE.size == ctypes.sizeof(_lib.sa_sink_shape)
+assert _PAGED_SHAPE.size == ctypes.sizeof(_lib.sa_paged_shape)
 
 
 class _on_device:
     """The device of a call made current, if it is not already."""
     __slots__ = ("index", "guard")
 
-    def __init__(self, dev):
-        self.index = dev.index
+    def __init__(self, index):
+        self.index = index
 
     def __enter__(self):
         self.guard = None
@@ -559,8 +567,15 @@ class _on_device:
             self.guard.__exit__(*exc)
 
 
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
 def _need_rows(t, name: str, dtype, dev, shape):
-    """A tensor of rows: any strides that are multiples of 16 bytes, the last dimension contiguous."""
+    """Refuses a tensor of rows that has not strides of multiples of 16 bytes and a contiguous last dimension."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
@@ -580,69 +595,81 @@ def _need_rows(t, name: str, dtype, dev, shape):
                 raise ValueError(f"{name}: strides must be multiples of 16 bytes, got {st}")
             if t.shape[i] > 1 and st[i] <= 0:
                 raise ValueError(f"{name}: a broadcast input is not supported, got strides {st}")
-    return t
 
 
-def _row_strides(t, n: int):
-    """Strides in front of the last dimension; a dimension of size 1 is never stepped over."""
-    return [s if size > 1 else 0 for s, size in zip(t.stride()[:n], t.shape[:n])]
+def _rows(t, name: str, dtype, dev, shape, mask: int = 7):
+    """Strides in front of the last dimension of a checked tensor of rows; mask: elements in 16 bytes, less 1.
+    A dimension of size 1 is never stepped over (its stride is given as 0 where it would not pass)."""
+    if t is not None and t.dtype == dtype and t.device == dev and t.shape == shape and not t.data_ptr() & 15:
+        st = t.stride()
+        if st[-1] == 1:
+            st, bad = st[:-1], False
+            for x in st:
+                if x <= 0 or x & mask:
+                    bad = True
+            if not bad:
+                return st
+    _need_rows(t, name, dtype, dev, shape)
+    return tuple(x if size > 1 else 0 for x, size in zip(t.stride()[:-1], t.shape))
 
 
-def _need_out(t, name: str, dtype, dev, shape):
+def _need_out(t, name: str, like, dtype, shape):
+    """The output given, checked, or a new one beside `like`."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need(t, name, dtype, dev)
+        if dtype == like.dtype and shape == like.shape and like.is_contiguous():
+            return torch.empty_like(like)
+        return like.new_empty(tuple(shape), dtype=dtype)
+    _need(t, name, dtype, like.device)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
 
+def _ints(t, name: str, dev, n=None):
+    """The length of a list int32 [n] on the device."""
+    if t is None or t.dtype != torch.int32 or t.device != dev or t.dim() != 1 or not t.is_contiguous():
+        _need(t, name, torch.int32, dev, 1)
+    m = t.shape[0]
+    if n is not None and m != n:
+        raise ValueError(f"{name} must have {n} entries, got {m}")
+    return m
+
+
 def _sink_shape(what, q, k, v, window, sinks, cu_q, cu_k, max_q, max_k, scale, q_pos0, dtypes):
+    """Checks the inputs; the fields of sa_sink_shape up to v_stride, the device, whether the batch is packed."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise ValueError(f"{what}: q must be a CUDA tensor (there is no CPU path)")
-    dev, dt = q.device, q.dtype
+    dev, dt, qs = q.device, q.dtype, q.shape
     if dt not in dtypes:
         raise TypeError(f"{what}: q must be one of {[str(x) for x in dtypes]}, got {dt}")
-    if (cu_q is None) != (cu_k is None):
-        raise ValueError(f"{what}: cu_q and cu_k go together")
     packed = cu_q is not None
-    if q.dim() != (3 if packed else 4) or k is None or k.dim() != q.dim():
+    if packed != (cu_k is not None):
+        raise ValueError(f"{what}: cu_q and cu_k go together")
+    if len(qs) != (3 if packed else 4) or k is None or k.dim() != len(qs):
         raise ValueError(f"{what}: q and k must have {3 if packed else 4} dims")
-    Hq, d = q.shape[-2:]
-    Hkv = k.shape[-2]
+    ks = k.shape
+    Hq, d = qs[-2:]
+    Hkv = ks[-2]
     if packed:
-        _need(cu_q, "cu_q", torch.int32, dev, 1)
-        _need(cu_k, "cu_k", torch.int32, dev, 1)
-        B, Tq, L = cu_q.shape[0] - 1, q.shape[0], k.shape[0]
-        if B < 1 or cu_k.shape != cu_q.shape:
+        B, Tq, L = _ints(cu_q, "cu_q", dev) - 1, qs[0], ks[0]
+        if B < 1 or _ints(cu_k, "cu_k", dev) != B + 1:
             raise ValueError(f"{what}: cu_q and cu_k must be int32 [B+1]")
         if q_pos0 is not None:
             raise ValueError(f"{what}: q_pos0 has no meaning for packed sequences")
         pos0, kshape = 0, (L, Hkv, d)
     else:
-        if max_q is not None and max_q != q.shape[1] or max_k is not None and max_k != k.shape[1]:
+        B, Tq, L = qs[0], qs[1], ks[1]
+        if max_q is not None and max_q != Tq or max_k is not None and max_k != L:
             raise ValueError(f"{what}: max_q and max_k of a dense batch are its lengths")
-        B, Tq, L = q.shape[0], q.shape[1], k.shape[1]
         pos0, kshape = L - Tq if q_pos0 is None else int(q_pos0), (B, L, Hkv, d)
+        if pos0 < 0:
+            raise ValueError(f"{what}: more queries than keys needs q_pos0")
         max_q = max_k = 0
-    _need_rows(q, "q", dt, dev, q.shape)
-    _need_rows(k, "k", dt, dev, kshape)
-    _need_rows(v, "v", dt, dev, kshape)
-    if not packed and pos0 < 0:
-        raise ValueError(f"{what}: more queries than keys needs q_pos0")
-    s = sa_sink_shape()
-    s.dtype, s.B, s.Hq, s.Hkv, s.d = _ATTN_TYPES[dt], B, Hq, Hkv, d
-    s.window, s.sinks = int(window), int(sinks)
-    s.scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    s.Tq, s.L, s.q_pos0, s.max_q, s.max_k = Tq, L, pos0, int(max_q or 0), int(max_k or 0)
-    for dst, t in ((s.q_stride, q), (s.k_stride, k), (s.v_stride, v)):
-        _set_strides(dst, t, packed)
-    return s, dev, packed
-
-
-def _set_strides(dst, t, packed):
-    """Batch, token and head strides of a tensor [B,T,H,...] (packed: [N,H,...])."""
-    dst[0], dst[1], dst[2] = [0, *_row_strides(t, 2)] if packed else _row_strides(t, 3)
+    lead = (0,) if packed else ()
+    st = (*lead, *_rows(q, "q", dt, dev, qs), *lead, *_rows(k, "k", dt, dev, kshape), *lead,
+          *_rows(v, "v", dt, dev, kshape))
+    return (_ATTN_TYPES[dt], B, Hq, Hkv, d, min(int(window), _INT_MAX), min(int(sinks), _INT_MAX), 1.0 / math.sqrt(d) if scale is None else scale,
+            Tq, L, pos0, max_q or 0, max_k or 0, *st), dev, packed
 
 
 def sink_attn_fwd(q, k, v, window: int, sinks: int = 0, cu_q=None, cu_k=None, max_q: Optional[int] = None,
@@ -658,13 +685,16 @@ def sink_attn_fwd(q, k, v, window: int, sinks: int = 0, cu_q=None, cu_k=None, ma
     outside every packed sequence are left as they were in `out` and `lse`.
     """
     lib = _lib.load()
-    s, dev, packed = _sink_shape("sink_attn_fwd", q, k, v, window, sinks, cu_q, cu_k, max_q, max_k, scale, q_pos0,
-                                 tuple(_ATTN_TYPES))
-    out = _need_out(out, "out", q.dtype, dev, q.shape)
-    lse = _need_out(lse, "lse", torch.float32, dev, q.shape[:-1])
-    with _on_device(dev):
-        check(lib.sa_sink_attn_fwd(ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(cu_q), _ptr(cu_k),
-                                   out.data_ptr(), lse.data_ptr(), _stream(dev)), "sa_sink_attn_fwd")
+    f, dev, packed = _sink_shape("sink_attn_fwd", q, k, v, window, sinks, cu_q, cu_k, max_q, max_k, scale, q_pos0,
+                                 _ATTN_TYPES)
+    qs = q.shape
+    out = _need_out(out, "out", q, q.dtype, qs)
+    lse = _need_out(lse, "lse", q, torch.float32, qs[:-1])
+    with _on_device(dev.index):
+        rc = lib.sa_sink_attn_fwd(_SINK_SHAPE.pack(*f, 0, 0, 0, 0, 0, 0), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                  _ptr(cu_q), _ptr(cu_k), out.data_ptr(), lse.data_ptr(), _raw_stream(dev.index))
+    if rc:
+        check(rc, "sa_sink_attn_fwd")
     return out, lse
 
 
@@ -674,28 +704,28 @@ def sink_attn_bwd(q, k, v, out, lse, dout, window: int, sinks: int = 0, cu_q=Non
     """Backward of sink_attn_fwd (sa_sink_attn_bwd), bf16.
 
     out and lse are the forward's (out may be None: only lse is read); the
-    other arguments as there.  Returns (dq, dk, dv), bf16, shaped like q, k and v; rows outside every packed
-    sequence are left as they were.
+    other arguments as there.  Returns (dq, dk, dv), bf16, shaped like q, k
+    and v; rows outside every packed sequence are left as they were.
     """
     lib = _lib.load()
-    s, dev, packed = _sink_shape("sink_attn_bwd", q, k, v, window, sinks, cu_q, cu_k, max_q, max_k, scale, q_pos0,
-                                 (torch.bfloat16,))
-    _need_rows(dout, "dout", torch.bfloat16, dev, q.shape)
+    bf = torch.bfloat16
+    f, dev, packed = _sink_shape("sink_attn_bwd", q, k, v, window, sinks, cu_q, cu_k, max_q, max_k, scale, q_pos0,
+                                 (bf,))
+    qs, lead = q.shape, (0,) if packed else ()
     if out is not None:
-        _need_rows(out, "out", torch.bfloat16, dev, q.shape)
-    if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or lse.device != dev or lse.shape != q.shape[:-1]:
+        _rows(out, "out", bf, dev, qs)
+    if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or lse.device != dev or lse.shape != qs[:-1]:
         raise ValueError("sink_attn_bwd: lse must be the forward's, fp32 and shaped like q without d")
-    for dst, t in ((s.dout_stride, dout), (s.lse_stride, lse)):
-        _set_strides(dst, t, packed)
-    dq = _need_out(dq, "dq", torch.bfloat16, dev, q.shape)
-    dk = _need_out(dk, "dk", torch.bfloat16, dev, k.shape)
-    dv = _need_out(dv, "dv", torch.bfloat16, dev, v.shape)
-    with _on_device(dev):
-        nbytes = lib.sa_sink_attn_bwd_workspace_size(ctypes.byref(s), int(packed))
-        ws = _workspace(nbytes, dev)
-        check(lib.sa_sink_attn_bwd(ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(out),
-                                   lse.data_ptr(), dout.data_ptr(), _ptr(cu_q), _ptr(cu_k), dq.data_ptr(),
-                                   dk.data_ptr(), dv.data_ptr(), _ptr(ws), nbytes, _stream(dev)), "sa_sink_attn_bwd")
+    shape = _SINK_SHAPE.pack(*f, *lead, *_rows(dout, "dout", bf, dev, qs), *lead, *lse.stride())
+    dq, dk, dv = _need_out(dq, "dq", q, bf, qs), _need_out(dk, "dk", k, bf, k.shape), _need_out(dv, "dv", v, bf, v.shape)
+    with _on_device(dev.index):
+        nbytes = lib.sa_sink_attn_bwd_workspace_size(shape, int(packed))
+        ws = q.new_empty(nbytes, dtype=torch.uint8)
+        rc = lib.sa_sink_attn_bwd(shape, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(out), lse.data_ptr(),
+                                  dout.data_ptr(), _ptr(cu_q), _ptr(cu_k), dq.data_ptr(), dk.data_ptr(),
+                                  dv.data_ptr(), _ptr(ws), nbytes, _raw_stream(dev.index))
+    if rc:
+        check(rc, "sa_sink_attn_bwd")
     return dq, dk, dv
 
 
@@ -712,38 +742,35 @@ def paged_attn_decode(q, k_cache, v_cache, block_table, seq_lens, window: Option
     lib = _lib.load()
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise ValueError("paged_attn_decode: q must be a CUDA tensor (there is no CPU path)")
-    dev, dt = q.device, q.dtype
+    dev, dt, qs = q.device, q.dtype, q.shape
     if dt not in _ATTN_TYPES:
         raise TypeError(f"paged_attn_decode: q must be bfloat16 or float16, got {dt}")
-    if q.dim() != 3 or k_cache is None or k_cache.dim() != 4:
+    if len(qs) != 3 or k_cache is None or k_cache.dim() != 4:
         raise ValueError("paged_attn_decode: q must be [B,Hq,d] and the caches [n_pages,page,Hkv,d]")
-    B, Hq, d = q.shape
+    B, Hq, d = qs
     n_pages, page, Hkv = k_cache.shape[:3]
-    _need_rows(q, "q", dt, dev, q.shape)
-    _need_rows(k_cache, "k_cache", dt, dev, (n_pages, page, Hkv, d))
-    _need_rows(v_cache, "v_cache", dt, dev, (n_pages, page, Hkv, d))
+    cs = (n_pages, page, Hkv, d)
+    st = (*_rows(q, "q", dt, dev, qs), *_rows(k_cache, "k_cache", dt, dev, cs), *_rows(v_cache, "v_cache", dt, dev, cs))
     _need(block_table, "block_table", torch.int32, dev, 2)
-    _need(seq_lens, "seq_lens", torch.int32, dev, 1)
-    if block_table.shape[0] != B or seq_lens.shape[0] != B:
+    if block_table.shape[0] != B or _ints(seq_lens, "seq_lens", dev) != B:
         raise ValueError("paged_attn_decode: block_table and seq_lens must have a row per sequence")
     if window is not None and window < 1:
         raise ValueError("paged_attn_decode: window >= 1 (None: every key)")
-    s = sa_paged_shape()
-    s.dtype, s.B, s.Hq, s.Hkv, s.d, s.page, s.max_pages = _ATTN_TYPES[dt], B, Hq, Hkv, d, page, block_table.shape[1]
-    s.window, s.sinks, s.n_pages = int(window or 0), int(sinks), n_pages
-    s.scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    s.q_stride[0], s.q_stride[1] = _row_strides(q, 2)
-    s.k_stride[0], s.k_stride[1], s.k_stride[2] = _row_strides(k_cache, 3)
-    s.v_stride[0], s.v_stride[1], s.v_stride[2] = _row_strides(v_cache, 3)
-    out = _need_out(out, "out", dt, dev, q.shape)
-    lse = _need_out(lse, "lse", torch.float32, dev, q.shape[:-1])
-    with _on_device(dev):
-        nbytes = lib.sa_paged_attn_decode_workspace_size(B, Hq, Hkv, d)
-        ws = workspace if workspace is not None else _workspace(nbytes, dev)
-        have = 0 if ws is None else ws.numel() * ws.element_size()
-        check(lib.sa_paged_attn_decode(ctypes.byref(s), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                       block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                       _ptr(ws), have, _stream(dev)), "sa_paged_attn_decode")
+    shape = _PAGED_SHAPE.pack(_ATTN_TYPES[dt], B, Hq, Hkv, d, page, block_table.shape[1],
+                              min(int(window or 0), _INT_MAX), min(int(sinks), _INT_MAX), 1.0 / math.sqrt(d) if scale is None else scale, n_pages, *st)
+    out = _need_out(out, "out", q, dt, qs)
+    lse = _need_out(lse, "lse", q, torch.float32, qs[:-1])
+    with _on_device(dev.index):
+        if workspace is None:
+            have = lib.sa_paged_attn_decode_workspace_size(B, Hq, Hkv, d)
+            workspace = q.new_empty(have, dtype=torch.uint8)
+        else:
+            have = workspace.numel() * workspace.element_size()
+        rc = lib.sa_paged_attn_decode(shape, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                      block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                      _ptr(workspace), have, _raw_stream(dev.index))
+    if rc:
+        check(rc, "sa_paged_attn_decode")
     return out, lse
 
 
@@ -756,54 +783,41 @@ def _books(what, block_table, refcount, seq_lens=None):
         raise ValueError(f"{what}: block_table is required")
     dev = block_table.device
     _need(block_table, "block_table", torch.int32, dev, 2)
-    _need(refcount, "refcount", torch.int32, dev, 1)
-    if seq_lens is not None:
-        _need(seq_lens, "seq_lens", torch.int32, dev, 1)
-        if seq_lens.shape[0] != block_table.shape[0]:
-            raise ValueError(f"{what}: block_table and seq_lens must have a row per sequence")
-    return dev, block_table.shape[0], block_table.shape[1], refcount.shape[0]
-
-
-def _list(t, name, dev, n=None):
-    _need(t, name, torch.int32, dev, 1)
-    if n is not None and t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
-    return t
+    S, max_pages = block_table.shape
+    if seq_lens is not None and _ints(seq_lens, "seq_lens", dev) != S:
+        raise ValueError(f"{what}: block_table and seq_lens must have a row per sequence")
+    return dev, S, max_pages, _ints(refcount, "refcount", dev)
 
 
 def _page_caches(what, caches, dev, n_pages, page):
     """Caches [n_pages, page, ...] of one slot size as the C array; (array, bytes per slot, page)."""
-    arr = (sa_page_cache * max(1, len(caches)))()
-    slot_bytes = 0
+    fields, slot_bytes = [], 0
     for i, c in enumerate(caches):
         if not isinstance(c, torch.Tensor) or c.dim() < 2 or c.device != dev:
             raise ValueError(f"{what}: caches must be tensors [n_pages, page, ...] on {dev}")
-        page = c.shape[1] if page is None else page
-        if c.shape[0] != n_pages or c.shape[1] != page:
-            raise ValueError(f"{what}: cache {i} must be [{n_pages}, {page}, ...], got {tuple(c.shape)}")
-        es = c.element_size()
-        n = math.prod(c.shape[2:])
-        want, inner = 1, True
-        for size, st in zip(reversed(c.shape[2:]), reversed(c.stride()[2:])):
-            inner = inner and (size == 1 or st == want)
-            want *= size
-        if not inner:
-            raise ValueError(f"{what}: the slots of cache {i} must be contiguous")
-        if i and n * es != slot_bytes:
+        shape, st, es = c.shape, c.stride(), c.element_size()
+        page = shape[1] if page is None else page
+        if shape[0] != n_pages or shape[1] != page:
+            raise ValueError(f"{what}: cache {i} must be [{n_pages}, {page}, ...], got {tuple(shape)}")
+        n = es
+        for size, x in zip(shape[:1:-1], st[:1:-1]):
+            if size != 1 and x * es != n:
+                raise ValueError(f"{what}: the slots of cache {i} must be contiguous")
+            n *= size
+        if i and n != slot_bytes:
             raise ValueError(f"{what}: the caches must have the same bytes per slot")
-        slot_bytes = n * es
-        st = c.stride()
-        arr[i].base, arr[i].page_stride = c.data_ptr(), st[0] * es if n_pages > 1 else 0
-        arr[i].slot_stride = st[1] * es if page > 1 else slot_bytes
+        slot_bytes = n
+        fields += c.data_ptr(), st[0] * es if n_pages > 1 else 0, st[1] * es if page > 1 else n
     if page is None:
         raise ValueError(f"{what}: page is required without caches")
-    return arr, slot_bytes, page
+    return struct.pack(f"={len(fields)}q", *fields), slot_bytes, page
 
 
-def _books_workspace(lib, S, n, n_pages, dev, workspace):
+def _books_workspace(lib, S, n, n_pages, like, workspace):
+    if workspace is not None:
+        return workspace, workspace.numel() * workspace.element_size()
     nbytes = lib.sa_paged_books_workspace_size(S, n, n_pages)
-    ws = workspace if workspace is not None else _workspace(nbytes, dev)
-    return ws, 0 if ws is None else ws.numel() * ws.element_size()
+    return like.new_empty(nbytes, dtype=torch.uint8), nbytes
 
 
 def paged_extend(block_table, seq_lens, refcount, seqs, n_new, page: int, start=None, workspace=None):
@@ -815,14 +829,16 @@ def paged_extend(block_table, seq_lens, refcount, seqs, n_new, page: int, start=
     """
     lib = _lib.load()
     dev, S, max_pages, n_pages = _books("paged_extend", block_table, refcount, seq_lens)
-    n = _list(seqs, "seqs", dev).shape[0]
-    _list(n_new, "n_new", dev, n)
-    start = _need_out(start, "start", torch.int32, dev, seqs.shape)
-    with _on_device(dev):
-        ws, have = _books_workspace(lib, S, n, n_pages, dev, workspace)
-        check(lib.sa_paged_extend(block_table.data_ptr(), seq_lens.data_ptr(), refcount.data_ptr(), S, max_pages,
-                                  n_pages, int(page), seqs.data_ptr(), n_new.data_ptr(), n, start.data_ptr(),
-                                  _ptr(ws), have, _stream(dev)), "sa_paged_extend")
+    n = _ints(seqs, "seqs", dev)
+    _ints(n_new, "n_new", dev, n)
+    start = _need_out(start, "start", seqs, torch.int32, (n,))
+    with _on_device(dev.index):
+        ws, have = _books_workspace(lib, S, n, n_pages, refcount, workspace)
+        rc = lib.sa_paged_extend(block_table.data_ptr(), seq_lens.data_ptr(), refcount.data_ptr(), S, max_pages,
+                                 n_pages, int(page), seqs.data_ptr(), n_new.data_ptr(), n, start.data_ptr(),
+                                 _ptr(ws), have, _raw_stream(dev.index))
+    if rc:
+        check(rc, "sa_paged_extend")
     return start
 
 
@@ -838,27 +854,28 @@ def paged_write(k_new, v_new, k_cache, v_cache, block_table, seqs, start, cu_new
     if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3 or not isinstance(k_cache, torch.Tensor) or \
             k_cache.dim() != 4:
         raise ValueError("paged_write: k_new must be [N,Hkv,d] and k_cache [n_pages,page,Hkv,d]")
-    dev, dt = k_new.device, k_new.dtype
-    N, Hkv, d = k_new.shape
+    dev, dt, es, ns = k_new.device, k_new.dtype, k_new.element_size(), k_new.shape
+    if not k_new.is_cuda:
+        raise ValueError("paged_write: k_new must be a CUDA tensor (there is no CPU path)")
+    N, Hkv, d = ns
     n_pages, page = k_cache.shape[:2]
-    _need_rows(k_new, "k_new", dt, dev, (N, Hkv, d))
-    _need_rows(v_new, "v_new", dt, dev, (N, Hkv, d))
-    _need_rows(k_cache, "k_cache", dt, dev, (n_pages, page, Hkv, d))
-    _need_rows(v_cache, "v_cache", dt, dev, (n_pages, page, Hkv, d))
+    cs, m = (n_pages, page, Hkv, d), 16 // es - 1
+    strides = struct.pack("=10q", *_rows(k_new, "k_new", dt, dev, ns, m), *_rows(v_new, "v_new", dt, dev, ns, m),
+                          *_rows(k_cache, "k_cache", dt, dev, cs, m), *_rows(v_cache, "v_cache", dt, dev, cs, m))
     _need(block_table, "block_table", torch.int32, dev, 2)
-    n = _list(seqs, "seqs", dev).shape[0]
-    _list(start, "start", dev, n)
+    n = _ints(seqs, "seqs", dev)
+    _ints(start, "start", dev, n)
     if cu_new is not None:
-        _list(cu_new, "cu_new", dev, n + 1)
+        _ints(cu_new, "cu_new", dev, n + 1)
     elif N != n:
         raise ValueError("paged_write: without cu_new one row per entry")
-    strides = [(ctypes.c_int64 * m)(*_row_strides(t, m)) for t, m in ((k_new, 2), (v_new, 2), (k_cache, 3),
-                                                                      (v_cache, 3))]
-    with _on_device(dev):
-        check(lib.sa_paged_write(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                 block_table.data_ptr(), seqs.data_ptr(), start.data_ptr(), _ptr(cu_new), n, N,
-                                 block_table.shape[0], block_table.shape[1], n_pages, page, Hkv, d,
-                                 k_new.element_size(), *strides, _stream(dev)), "sa_paged_write")
+    S, max_pages = block_table.shape
+    with _on_device(dev.index):
+        rc = lib.sa_paged_write(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                block_table.data_ptr(), seqs.data_ptr(), start.data_ptr(), _ptr(cu_new), n, N, S,
+                                max_pages, n_pages, page, Hkv, d, es, strides, _raw_stream(dev.index))
+    if rc:
+        check(rc, "sa_paged_write")
 
 
 def paged_fork(block_table, seq_lens, refcount, src, dst, page: int, caches=(), done=None, workspace=None):
@@ -869,15 +886,17 @@ def paged_fork(block_table, seq_lens, refcount, src, dst, page: int, caches=(), 
     """
     lib = _lib.load()
     dev, S, max_pages, n_pages = _books("paged_fork", block_table, refcount, seq_lens)
-    n = _list(src, "src", dev).shape[0]
-    _list(dst, "dst", dev, n)
+    n = _ints(src, "src", dev)
+    _ints(dst, "dst", dev, n)
     arr, slot_bytes, page = _page_caches("paged_fork", caches, dev, n_pages, int(page))
-    done = _need_out(done, "done", torch.int32, dev, src.shape)
-    with _on_device(dev):
-        ws, have = _books_workspace(lib, S, n, n_pages, dev, workspace)
-        check(lib.sa_paged_fork(block_table.data_ptr(), seq_lens.data_ptr(), refcount.data_ptr(), S, max_pages,
-                                n_pages, page, src.data_ptr(), dst.data_ptr(), n, arr, len(caches), slot_bytes,
-                                done.data_ptr(), _ptr(ws), have, _stream(dev)), "sa_paged_fork")
+    done = _need_out(done, "done", src, torch.int32, (n,))
+    with _on_device(dev.index):
+        ws, have = _books_workspace(lib, S, n, n_pages, refcount, workspace)
+        rc = lib.sa_paged_fork(block_table.data_ptr(), seq_lens.data_ptr(), refcount.data_ptr(), S, max_pages, n_pages,
+                               page, src.data_ptr(), dst.data_ptr(), n, arr, len(caches), slot_bytes, done.data_ptr(),
+                               _ptr(ws), have, _raw_stream(dev.index))
+    if rc:
+        check(rc, "sa_paged_fork")
     return done
 
 
@@ -887,13 +906,15 @@ def paged_free(block_table, seq_lens, refcount, seqs, page: Optional[int] = None
     those that no later query can see (sa_paged_free; page is needed then)."""
     lib = _lib.load()
     dev, S, max_pages, n_pages = _books("paged_free", block_table, refcount, seq_lens)
-    n = _list(seqs, "seqs", dev).shape[0]
+    n = _ints(seqs, "seqs", dev)
     if window is not None and (window < 1 or page is None):
         raise ValueError("paged_free: a window needs window >= 1 and page")
-    with _on_device(dev):
-        check(lib.sa_paged_free(block_table.data_ptr(), seq_lens.data_ptr(), refcount.data_ptr(), S, max_pages,
-                                n_pages, int(page or 1), seqs.data_ptr(), n, int(window or 0), int(sinks),
-                                _stream(dev)), "sa_paged_free")
+    with _on_device(dev.index):
+        rc = lib.sa_paged_free(block_table.data_ptr(), seq_lens.data_ptr(), refcount.data_ptr(), S, max_pages, n_pages,
+                               int(page or 1), seqs.data_ptr(), n, min(int(window or 0), _INT_MAX),
+                               min(int(sinks), _INT_MAX), _raw_stream(dev.index))
+    if rc:
+        check(rc, "sa_paged_free")
 
 
 def paged_compact(block_table, refcount, caches=(), page: Optional[int] = None, n_live=None, workspace=None):
@@ -905,10 +926,11 @@ def paged_compact(block_table, refcount, caches=(), page: Optional[int] = None, 
     lib = _lib.load()
     dev, S, max_pages, n_pages = _books("paged_compact", block_table, refcount)
     arr, slot_bytes, page = _page_caches("paged_compact", caches, dev, n_pages, page if caches else (page or 1))
-    n_live = _need_out(n_live, "n_live", torch.int32, dev, (1,))
-    with _on_device(dev):
-        ws, have = _books_workspace(lib, S, 0, n_pages, dev, workspace)
-        check(lib.sa_paged_compact(block_table.data_ptr(), refcount.data_ptr(), S, max_pages, n_pages, page, arr,
-                                   len(caches), slot_bytes, n_live.data_ptr(), _ptr(ws), have, _stream(dev)),
-              "sa_paged_compact")
+    n_live = _need_out(n_live, "n_live", refcount, torch.int32, (1,))
+    with _on_device(dev.index):
+        ws, have = _books_workspace(lib, S, 0, n_pages, refcount, workspace)
+        rc = lib.sa_paged_compact(block_table.data_ptr(), refcount.data_ptr(), S, max_pages, n_pages, page, arr,
+                                  len(caches), slot_bytes, n_live.data_ptr(), _ptr(ws), have, _raw_stream(dev.index))
+    if rc:
+        check(rc, "sa_paged_compact")
     return n_live

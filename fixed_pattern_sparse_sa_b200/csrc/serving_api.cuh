@@ -11,6 +11,18 @@
 #include "sink_fwd_tc.cuh"
 
 // ---------------------------------------------------- sink-window attention --
+// set_smem once per device: `done` (one bit a device) belongs to one kernel.
+template <typename K>
+static int set_smem_once(std::atomic<unsigned long long> &done, K kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return fail(SA_ERR_CUDA, "cudaGetDevice: device %d", dev);
+    const unsigned long long bit = 1ull << dev;
+    if (done.load(std::memory_order_relaxed) & bit) return SA_OK;
+    const int rc = set_smem(kernel, bytes);
+    if (rc == SA_OK) done.fetch_or(bit, std::memory_order_relaxed);
+    return rc;
+}
 static bool strides_ok(const int64_t *s, int n, long long mul) {
     for (int i = 0; i < n; ++i)
         if (s[i] < 0 || s[i] % mul) return false;
@@ -119,7 +131,8 @@ static int sink_fwd_launch(const SinkParams &p, cudaStream_t st) {
     int rc = rows_tensor_map<T>(&qm, p.q, D, p.Hq, p.Tq, nb, p.q_s, t.HB, t.TPT);
     if (!rc) rc = rows_tensor_map<T>(&km, k, D, p.Hkv, std::max(p.L, 1ll), nb, p.k_s, 1, SF_KT);
     if (!rc) rc = rows_tensor_map<T>(&vm, v, D, p.Hkv, std::max(p.L, 1ll), nb, p.v_s, 1, SF_KT);
-    if (!rc) rc = set_smem(sink_fwd_tc_kernel<T, D>, SfSmem<D>::ALLOC);
+    static std::atomic<unsigned long long> done{0};
+    if (!rc) rc = set_smem_once(done, sink_fwd_tc_kernel<T, D>, SfSmem<D>::ALLOC);
     if (rc) return rc;
     const unsigned grid = (unsigned)std::min<long long>(t.items, sm_count());
     launch_k("sink_fwd_tc_kernel", sink_fwd_tc_kernel<T, D>, grid, SF_THREADS, SfSmem<D>::ALLOC, st, qm, km, vm, p, t);
@@ -209,7 +222,8 @@ static int sink_bwd_launch(const SinkParams &p, void *ws, cudaStream_t st) {
         const SinkTiles t = sink_tiles(p, 1);
         rc = rows_tensor_map<T>(&qm, q, D, p.Hq, Tq, nb, p.q_s, t.HB, t.TPT);
         if (!rc) rc = rows_tensor_map<T>(&gm, g, D, p.Hq, Tq, nb, p.do_s, t.HB, t.TPT);
-        if (!rc) rc = set_smem(sink_dq_tc_kernel<D>, SqSmem<D>::ALLOC);
+        static std::atomic<unsigned long long> done{0};
+        if (!rc) rc = set_smem_once(done, sink_dq_tc_kernel<D>, SqSmem<D>::ALLOC);
         if (rc) return rc;
         const unsigned grid = (unsigned)std::min(t.items, sm_count());
         launch_k("sink_dq_tc_kernel", sink_dq_tc_kernel<D>, grid, SB_THREADS, SqSmem<D>::ALLOC, st, qm, gm, km, vm, p, t,
@@ -222,7 +236,8 @@ static int sink_bwd_launch(const SinkParams &p, void *ws, cudaStream_t st) {
     if (p.L > 0) {
         rc = rows_tensor_map<T>(&qm, q, D, p.Hq, Tq, nb, p.q_s, kt.HB, kt.TPT);
         if (!rc) rc = rows_tensor_map<T>(&gm, g, D, p.Hq, Tq, nb, p.do_s, kt.HB, kt.TPT);
-        if (!rc) rc = set_smem(sink_dkv_tc_kernel<D>, SkSmem<D>::ALLOC);
+        static std::atomic<unsigned long long> done{0};
+        if (!rc) rc = set_smem_once(done, sink_dkv_tc_kernel<D>, SkSmem<D>::ALLOC);
         if (rc) return rc;
         const unsigned grid = (unsigned)std::min(std::max(kt.items, 1), sm_count());
         launch_k("sink_dkv_tc_kernel", sink_dkv_tc_kernel<D>, grid, SB_THREADS, SkSmem<D>::ALLOC, st, qm, gm, km, vm, p,
@@ -282,7 +297,8 @@ extern "C" size_t sa_paged_attn_decode_workspace_size(int B, int Hq, int Hkv, in
 template <typename T, int D>
 static int pd_launch(const PagedParams &p, cudaStream_t st) {
     const int smem = PdSmem<D>::TOTAL, gx = pd_grid<D>();
-    int rc = set_smem(paged_decode_kernel<T, D>, smem);
+    static std::atomic<unsigned long long> done{0};
+    int rc = set_smem_once(done, paged_decode_kernel<T, D>, smem);
     if (rc) return rc;
     launch_k("paged_decode_kernel", paged_decode_kernel<T, D>, gx, PD_THREADS, smem, st, p);
     SA_CHECK_LAUNCH("paged_decode_kernel");
@@ -462,11 +478,10 @@ extern "C" int sa_paged_extend(int32_t *block_table, int32_t *seq_lens, int32_t 
 extern "C" int sa_paged_write(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
                               const int32_t *block_table, const int32_t *seqs, const int32_t *start,
                               const int32_t *cu_new, int n, int64_t N, int S, int max_pages, int64_t n_pages, int page,
-                              int Hkv, int d, int elem_bytes, const int64_t *k_new_stride, const int64_t *v_new_stride,
-                              const int64_t *k_stride, const int64_t *v_stride, void *stream) {
+                              int Hkv, int d, int elem_bytes, const int64_t *strides, void *stream) {
     SA_TRACE("sa_paged_write");
     if (n < 0 || N < 0 || S < 0 || max_pages < 0 || n_pages < 0 || page <= 0 || Hkv <= 0 || d <= 0 || elem_bytes <= 0 ||
-        !k_new_stride || !v_new_stride || !k_stride || !v_stride || (!cu_new && N != n))
+        !strides || (!cu_new && N != n))
         return fail(SA_ERR_INVALID_ARG, "paged_write: bad sizes (without cu_new one row per entry)");
     if ((long long)d * elem_bytes % 16 || (long long)Hkv * d * elem_bytes >= (1 << 28))
         return fail(SA_ERR_UNSUPPORTED, "paged_write: rows of %lld bytes (a multiple of 16)", (long long)d * elem_bytes);
@@ -478,7 +493,7 @@ extern "C" int sa_paged_write(const void *k_new, const void *v_new, void *k_cach
     PagedWriteParams p{};
     const void *src[2] = {k_new, v_new};
     void *dst[2] = {k_cache, v_cache};
-    const int64_t *ss[2] = {k_new_stride, v_new_stride}, *ds[2] = {k_stride, v_stride};
+    const int64_t *ss[2] = {strides, strides + 2}, *ds[2] = {strides + 4, strides + 7};
     for (int i = 0; i < 2; ++i) {
         p.src[i] = static_cast<const char *>(src[i]);
         p.dst[i] = static_cast<char *>(dst[i]);

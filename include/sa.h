@@ -485,9 +485,10 @@ int sa_paged_attn_decode(const sa_paged_shape *shape, const void *q, const void 
  * sa_paged_write: row r of k_new / v_new [N, Hkv, d], of list entry i (cu_new
  *   int32 [n+1], cu_new[i] <= r < cu_new[i+1]; NULL: N = n, one row each) goes
  *   to position start[i] + r - cu_new[i] of seqs[i]; entries with start < 0
- *   and rows outside cu_new are skipped.  Elements of elem_bytes bytes, d *
- *   elem_bytes and all strides (in elements; new: token, head; caches: page,
- *   slot, head) multiples of 16 bytes.
+ *   and rows outside cu_new are skipped.  Elements of elem_bytes bytes;
+ *   strides (host, int64 [10], elements): token, head of k_new and of v_new,
+ *   page, slot, head of k_cache and of v_cache.  They and d * elem_bytes are
+ *   multiples of 16 bytes.
  * sa_paged_fork: sequence dst[i] (length 0 before) becomes a copy of src[i]:
  *   full pages are shared (refcount + 1), a last page that is not full is
  *   copied in each of the n_caches caches to a fresh page, taken as in
@@ -521,8 +522,8 @@ int sa_paged_extend(int32_t *block_table, int32_t *seq_lens, int32_t *refcount, 
                     size_t workspace_bytes, void *stream);
 int sa_paged_write(const void *k_new, const void *v_new, void *k_cache, void *v_cache, const int32_t *block_table,
                    const int32_t *seqs, const int32_t *start, const int32_t *cu_new, int n, int64_t N, int S,
-                   int max_pages, int64_t n_pages, int page, int Hkv, int d, int elem_bytes, const int64_t *k_new_stride,
-                   const int64_t *v_new_stride, const int64_t *k_stride, const int64_t *v_stride, void *stream);
+                   int max_pages, int64_t n_pages, int page, int Hkv, int d, int elem_bytes, const int64_t *strides,
+                   void *stream);
 int sa_paged_fork(int32_t *block_table, int32_t *seq_lens, int32_t *refcount, int S, int max_pages, int64_t n_pages,
                   int page, const int32_t *src, const int32_t *dst, int n, const sa_page_cache *caches, int n_caches,
                   int64_t slot_bytes, int32_t *done, void *workspace, size_t workspace_bytes, void *stream);

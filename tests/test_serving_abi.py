@@ -144,13 +144,13 @@ def test_books(lib):
 
 
 def test_write(lib):
-    good = [(ctypes.c_int64 * 3)(2048, 128, 64)] * 4
+    good = (ctypes.c_int64 * 10)(128, 64, 128, 64, 2048, 128, 64, 2048, 128, 64)
+    odd = (ctypes.c_int64 * 10)(128, 64, 128, 64, 2048, 4, 64, 2048, 128, 64)
 
     def write(kn=P, kc=P, table=P, seqs=P, start=P, cu=N, n=3, rows=3, page=16, d=64, es=2, strides=good):
-        return lib.sa_paged_write(kn, P, kc, P, table, seqs, start, cu, n, rows, 4, 8, 100, page, 2, d, es, *strides,
-                                  None)
+        return lib.sa_paged_write(kn, P, kc, P, table, seqs, start, cu, n, rows, 4, 8, 100, page, 2, d, es, strides, None)
     for kw in (dict(kn=N), dict(kc=ODD), dict(table=N), dict(seqs=N), dict(start=ODD), dict(cu=ODD), dict(rows=4),
-               dict(page=0), dict(n=-1), dict(strides=[good[0], (ctypes.c_int64 * 3)(2048, 4, 64), good[0], good[0]])):
+               dict(page=0), dict(n=-1), dict(strides=odd), dict(strides=None)):
         assert write(**kw) == INVALID, kw
     assert write(d=4) == UNSUPPORTED
     assert write(n=0, rows=0, kn=N, seqs=N, start=N) == OK
