@@ -159,8 +159,9 @@ extern "C" int sa_sink_attn_fwd(const sa_sink_shape *shape, const void *q, const
 }
 
 // Key-major items of the backward and how the sinks' are cut: pieces of a
-// quarter of a band item, so that they fill the last wave, but of 32 units at
-// least, 64 pieces at most, and no more than four waves of them in all.
+// quarter of a band item, so that they fill the last wave, but of 4 units at
+// least (one piece of 32 units made a call on 512 tokens 33 us long), 64
+// pieces at most, and no more than four waves of them in all.
 static SinkKvTiles sink_kv_tiles(const SinkParams &p) {
     SinkKvTiles t{};
     t.HB = std::min(p.G, 64);
@@ -176,7 +177,7 @@ static SinkKvTiles sink_kv_tiles(const SinkParams &p) {
     t.n_split = 1;
     t.tps = (int)std::max<long long>(nq, 1);
     if (t.n_kt && nq) {
-        const long long want = std::max({(32ll * t.TPT + t.HC - 1) / t.HC, (p.window + 131ll) / 4, (nq + 63) / 64});
+        const long long want = std::max({(4ll * t.TPT + t.HC - 1) / t.HC, (p.window + 131ll) / 4, (nq + 63) / 64});
         const long long most = std::max<long long>(1, 4ll * 148 / ((long long)p.B * p.Hkv * t.n_kt));
         t.n_split = (int)std::min(most, (nq + want - 1) / want);
         t.tps = (int)((nq + t.n_split - 1) / t.n_split);
@@ -245,8 +246,8 @@ static int sink_bwd_launch(const SinkParams &p, void *ws, cudaStream_t st) {
         SA_CHECK_LAUNCH("sink_dkv_tc_kernel");
         if (kt.n_split > 1) {
             const long long jr = (long long)p.B * p.Hkv * p.sinks;
-            launch_k("sink_dkv_join_kernel", sink_dkv_join_kernel<D>, (unsigned)std::min<long long>((jr + 3) / 4, 1 << 20),
-                     128, 0, st, p, kt);
+            launch_k("sink_dkv_join_kernel", sink_dkv_join_kernel<D>, (unsigned)std::min<long long>(jr, 1 << 20), 256, 0, st,
+                     p, kt);
             SA_CHECK_LAUNCH("sink_dkv_join_kernel");
         }
     }

@@ -935,22 +935,25 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     if (warp == 9) tc::tmem_dealloc(tmem, 512);
 }
 
-// dk and dv of the sinks that lie apart: the pieces' fp32 sums in order, one
-// warp per key and KV head.
+// dk and dv of the sinks that lie apart: the pieces' fp32 sums, one CTA per
+// key and KV head; warp w takes pieces w, w + 8, ..., then the eight partial
+// sums are added in order.
 template <int D>
-__global__ void __launch_bounds__(128) sink_dkv_join_kernel(const SinkParams p, const SinkKvTiles tl) {
+__global__ void __launch_bounds__(256) sink_dkv_join_kernel(const SinkParams p, const SinkKvTiles tl) {
     grid_dependency_sync();
     constexpr int E = 2 * D / 32;
-    const int lane = threadIdx.x & 31;
+    __shared__ float sums[8][2 * D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long rows = (long long)p.B * p.Hkv * p.sinks;
-    for (long long w = blockIdx.x * 4ll + (threadIdx.x >> 5); w < rows; w += gridDim.x * 4ll) {
+    for (long long w = blockIdx.x; w < rows; w += gridDim.x) {
         const int j = (int)(w % p.sinks);
         const long long bh = w / p.sinks;
         const int hk = (int)(bh % p.Hkv), b = (int)(bh / p.Hkv);
         const SinkSeq s = sink_seq(p, b);
         if (j >= sink_apart(p, s)) continue;
         float x[E] = {};
-        for (int sp = 0; sp < tl.n_split; ++sp) {
+#pragma unroll 4
+        for (int sp = warp; sp < tl.n_split; sp += 8) {
             int ta, te;
             sink_piece(s, tl.tps, sp, j / 128 * 128, ta, te);
             if (ta >= te) continue;
@@ -962,11 +965,19 @@ __global__ void __launch_bounds__(128) sink_dkv_join_kernel(const SinkParams p, 
                 x[e] += v.x; x[e + 1] += v.y; x[e + 2] += v.z; x[e + 3] += v.w;
             }
         }
-        // lanes 0-15 hold dv, 16-31 dk
-        __nv_bfloat16 *out = (__nv_bfloat16 *)(lane < 16 ? p.dv : p.dk) +
-                             ((p.cu_k ? 0 : b * p.L) + s.k0 + j) * p.Hkv * D + (long long)hk * D + (lane & 15) * E;
 #pragma unroll
-        for (int e = 0; e < E; e += 2) *reinterpret_cast<unsigned *>(out + e) = pack_bf16(x[e], x[e + 1]);
+        for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = x[e];
+        __syncthreads();
+        // columns 0 .. D-1 are dv, the rest dk
+        const int c = threadIdx.x;
+        if (c < 2 * D) {
+            float y = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y += sums[i][c];
+            const long long row = (((p.cu_k ? 0 : b * p.L) + s.k0 + j) * p.Hkv + hk) * D;
+            ((__nv_bfloat16 *)(c < D ? p.dv : p.dk))[row + c % D] = __float2bfloat16(y);
+        }
+        __syncthreads();
     }
 }
 
