@@ -14,7 +14,6 @@ NVCC_FLAGS = [
     "-std=c++17", "-O3", "-lineinfo",
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-Xcompiler", "-fPIC", "-shared",
-    "--split-compile=0",             # the kernels of the one source file on all host cores
 ]
 
 

@@ -110,6 +110,15 @@ static int rows_tensor_map(CUtensorMap *m, const void *base, int d, long long he
     return SA_OK;
 }
 
+template <typename T>
+static int key_maps(KeyMaps &m, const void *base, int d, int heads, long long L, long long batch, const long long *st) {
+    L = std::max(L, 1ll);
+    int rc = rows_tensor_map<T>(&m.all, base, d, heads, L, batch, st, 1, SF_KT);
+    if (!rc) rc = rows_tensor_map<T>(&m.head, base, d, heads, L, batch, st, 1, SF_HEAD);
+    if (!rc) rc = rows_tensor_map<T>(&m.rest, base, d, heads, L, batch, st, 1, SF_KT - SF_HEAD);
+    return rc;
+}
+
 static SinkTiles sink_tiles(const SinkParams &p, int row_tiles) {
     SinkTiles t{};
     t.HB = std::min(p.G, 128);
@@ -125,12 +134,13 @@ template <typename T, int D>
 static int sink_fwd_launch(const SinkParams &p, cudaStream_t st) {
     const SinkTiles t = sink_tiles(p, 2);
     const long long nb = p.cu_q ? 1 : p.B;
-    CUtensorMap qm, km, vm;
+    CUtensorMap qm;
+    KeyMaps km, vm;
     // without keys nothing is loaded; the maps only have to be valid
     const void *k = p.L ? p.k : p.q, *v = p.L ? p.v : p.q;
     int rc = rows_tensor_map<T>(&qm, p.q, D, p.Hq, p.Tq, nb, p.q_s, t.HB, t.TPT);
-    if (!rc) rc = rows_tensor_map<T>(&km, k, D, p.Hkv, std::max(p.L, 1ll), nb, p.k_s, 1, SF_KT);
-    if (!rc) rc = rows_tensor_map<T>(&vm, v, D, p.Hkv, std::max(p.L, 1ll), nb, p.v_s, 1, SF_KT);
+    if (!rc) rc = key_maps<T>(km, k, D, p.Hkv, p.L, nb, p.k_s);
+    if (!rc) rc = key_maps<T>(vm, v, D, p.Hkv, p.L, nb, p.v_s);
     static std::atomic<unsigned long long> done{0};
     if (!rc) rc = set_smem_once(done, sink_fwd_tc_kernel<T, D>, SfSmem<D>::ALLOC);
     if (rc) return rc;
@@ -214,9 +224,10 @@ static int sink_bwd_launch(const SinkParams &p, void *ws, cudaStream_t st) {
     // an empty side is never loaded: its maps only have to be valid
     const void *any = p.Tq ? p.q : p.k, *q = any, *g = p.Tq ? p.dout : any, *k = p.L ? p.k : any, *v = p.L ? p.v : any;
     const long long Tq = std::max(p.Tq, 1ll), L = std::max(p.L, 1ll);
-    CUtensorMap km, vm, qm, gm;
-    int rc = rows_tensor_map<T>(&km, k, D, p.Hkv, L, nb, p.k_s, 1, 128);
-    if (!rc) rc = rows_tensor_map<T>(&vm, v, D, p.Hkv, L, nb, p.v_s, 1, 128);
+    CUtensorMap qm, gm;
+    KeyMaps km, vm;
+    int rc = key_maps<T>(km, k, D, p.Hkv, L, nb, p.k_s);
+    if (!rc) rc = key_maps<T>(vm, v, D, p.Hkv, L, nb, p.v_s);
     if (rc) return rc;
     // first: it also writes the rows' lse and D for the key-major pass, and resets its counter
     if (p.Tq > 0) {
@@ -241,7 +252,7 @@ static int sink_bwd_launch(const SinkParams &p, void *ws, cudaStream_t st) {
         if (!rc) rc = set_smem_once(done, sink_dkv_tc_kernel<D>, SkSmem<D>::ALLOC);
         if (rc) return rc;
         const unsigned grid = (unsigned)std::min(std::max(kt.items, 1), sm_count());
-        launch_k("sink_dkv_tc_kernel", sink_dkv_tc_kernel<D>, grid, SB_THREADS, SkSmem<D>::ALLOC, st, qm, gm, km, vm, p,
+        launch_k("sink_dkv_tc_kernel", sink_dkv_tc_kernel<D>, grid, SB_THREADS, SkSmem<D>::ALLOC, st, qm, gm, km.all, vm.all, p,
                  kt);
         SA_CHECK_LAUNCH("sink_dkv_tc_kernel");
         if (kt.n_split > 1) {

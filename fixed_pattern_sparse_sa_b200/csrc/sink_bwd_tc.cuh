@@ -37,7 +37,7 @@ constexpr int SB_REGS_SCORE = 208, SB_REGS_ISSUE = 88;     // as in the forward:
 //
 // Warps: 0-7 score and epilogue (thread = row; warps 0-3 the first 64 keys of
 // a tile, 4-7 the rest), 8 TMA producer, 9 MMA issuer of S and dP and TMEM
-// owner, 10 MMA issuer of dq.
+// owner, 10 MMA issuer of dq, 11 TMA producer of V.
 // beside the forward's tile facts: a tile of the walk for D, the first of the walk for dq
 enum : uint32_t { TI_SUM = 512u, TI_START = 1024u };
 constexpr uint32_t DQT_S = 0, DQT_DP = 256, DQT_DQ = 384;
@@ -49,9 +49,9 @@ struct SqSmem {
     static constexpr int OFF_K = OFF_Q + 4 * TILE;         // 2
     static constexpr int OFF_V = OFF_K + 2 * TILE;         // 1
     static constexpr int OFF_BAR = OFF_V + TILE;
-    // q_full[2], q_empty[2], k_full[2], k_empty[2], v_full, v_empty, s_full[2], dp_full, dp_free, ds_full[2],
+    // q_full[2], q_empty[2], k_full[2], k_empty[2], v_full, v_empty, dp_full, dp_free, ds_full[2],
     // dq_full, drain[2], item_full[2], item_empty[2]
-    static constexpr int N_BAR = 24;
+    static constexpr int N_BAR = 22;
     static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;   // tmem slot, abort flag, -, -, tile info[2]
     static constexpr int OFF_ITEM = OFF_MISC + 32;
     static constexpr int OFF_D = OFF_ITEM + 2 * 64;        // [2][128] halves of D
@@ -63,7 +63,7 @@ struct SqSmem {
 template <int D>
 __global__ void __launch_bounds__(SB_THREADS, 1)
     sink_dq_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap domap,
-                      const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                      const __grid_constant__ KeyMaps kmap, const __grid_constant__ KeyMaps vmap,
                       const __grid_constant__ SinkParams p, const __grid_constant__ SinkTiles tl, int *counter) {
     grid_dependency_sync();
     using T = __nv_bfloat16;
@@ -73,8 +73,8 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     unsigned char *smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
     uint64_t *q_full = bars, *q_empty = bars + 2, *k_full = bars + 4, *k_empty = bars + 6, *v_full = bars + 8;
-    uint64_t *v_empty = bars + 9, *s_full = bars + 10, *dp_full = bars + 12, *dp_free = bars + 13, *ds_full = bars + 14;
-    uint64_t *dq_full = bars + 16, *drain = bars + 17, *item_full = bars + 19, *item_empty = bars + 21;
+    uint64_t *v_empty = bars + 9, *dp_full = bars + 10, *dp_free = bars + 11, *ds_full = bars + 12;
+    uint64_t *dq_full = bars + 14, *drain = bars + 15, *item_full = bars + 17, *item_empty = bars + 19;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
     volatile uint32_t *info_s = reinterpret_cast<volatile uint32_t *>(smem + L::OFF_MISC + 16);
@@ -88,14 +88,14 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     if (tid == 0) {
         if (blockIdx.x == 0) *counter = 0;            // the key-major pass's next item
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(q_full + i, 1); tc::mbar_init(q_empty + i, 256);
+            tc::mbar_init(q_full + i, 1); tc::mbar_init(q_empty + i, 8);
             tc::mbar_init(k_full + i, 1); tc::mbar_init(k_empty + i, 1);
-            tc::mbar_init(s_full + i, 1); tc::mbar_init(ds_full + i, 256);
+            tc::mbar_init(ds_full + i, 8);
             tc::mbar_init(drain + i, 1);
-            tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 256);
+            tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 8);
         }
         tc::mbar_init(v_full, 1); tc::mbar_init(v_empty, 1);
-        tc::mbar_init(dp_full, 1); tc::mbar_init(dp_free, 256);
+        tc::mbar_init(dp_full, 1); tc::mbar_init(dp_free, 8);
         tc::mbar_init(dq_full, 1);
         *abort_flag = 0;
         tc::mbar_fence_init();
@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
             for (int it = blockIdx.x; it < tl.items && ok; it += gridDim.x) {
                 SinkItem x;
                 if (!sink_item<1>(p, tl, it, x)) continue;
-                ok = hand_over(SfItem{x.nt, {x.nq_i[0], 0}, (int)x.s.pos0 + x.t0, x.band_lo, x.band_hi, x.s_end, x.n_sink,
+                ok = hand_over(SfItem{x.nt, {x.nq_i[0], 0}, (int)x.s.pos0 + x.t0, x.band_lo, x.band_hi, x.s_end,
+                                      x.n_sink | x.head / SF_HEAD << 28,
                                       {0, 0}, {0, 0}, 0, 0, x.h0 | x.nh << 20,
                                       (int)((p.cu_q ? 0 : x.b * p.Tq) + x.s.q0) + x.t0});
                 if (!ok) break;
@@ -151,17 +152,10 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                     info_s[sl] = (uint32_t)((n + 15) / 16) | (i == 0 ? TI_FIRST : 0u) | (sum ? TI_SUM : 0u) |
                                  (i == x.nt ? TI_START : 0u) | (i + 1 == 2 * x.nt ? TI_LAST : 0u) | TI_TILE;
                     atc::expect_tx(k_full + sl, L::TILE);
-                    for (int h = 0; h < HALVES; ++h)
-                        load_4d(smem + L::OFF_K + sl * L::TILE + h * (128 * 128), &kmap, h * 64, x.hk,
-                                (int)(x.s.k0 + k0), cb, k_full + sl);
-                    if (!(ok = atc::wait(v_empty, (t & 1) ^ 1, abort_flag))) { ++t; break; }
-                    atc::expect_tx(v_full, L::TILE);
-                    for (int h = 0; h < HALVES; ++h)
-                        load_4d(smem + L::OFF_V + h * (128 * 128), &vmap, h * 64, x.hk, (int)(x.s.k0 + k0), cb, v_full);
+                    load_keys<D>(smem + L::OFF_K + sl * L::TILE, kmap, x, j, k0, cb, k_full + sl);
                 }
             }
             if (ok) ok = hand_over(SfItem{-1});
-            const int nv = t;
             if (ok) ok = atc::wait(k_empty + (t & 1), ((t >> 1) & 1) ^ 1, abort_flag);
             if (ok) {
                 info_s[t & 1] = 0u;
@@ -169,16 +163,31 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                 ++t;
             }
             if (!ok) fail();
-            // let the copies land before the CTA exits (after a failure V may be one tile behind)
+            // let the copies land before the CTA exits
             for (int i = 1; i <= 2 && i <= qn; ++i)
                 tc::mbar_wait_bounded(q_full + ((qn - i) & 1), ((qn - i) >> 1) & 1, ATC_WAIT);
             for (int i = 1; i <= 2 && i <= t; ++i)
                 tc::mbar_wait_bounded(k_full + ((t - i) & 1), ((t - i) >> 1) & 1, ATC_WAIT);
-            if (ok && nv > 0) tc::mbar_wait_bounded(v_full, (nv - 1) & 1, ATC_WAIT);
-            if (!ok && nv > 0) {
-                tc::mbar_wait_bounded(v_full, (nv - 1) & 1, ATC_WAIT / 8);
-                tc::mbar_wait_bounded(v_full, nv & 1, ATC_WAIT / 8);
+        } else if (warp == 11 && lane == 0) {
+            // ---------------------------------------------------- V producer
+            // its one buffer is free as soon as dP is formed, long before K's: a producer that
+            // waited for both in turn would hold the next K back
+            bool ok = true;
+            int t = 0;
+            for (int it = blockIdx.x; it < tl.items && ok; it += gridDim.x) {
+                SinkItem x;
+                if (!sink_item<1>(p, tl, it, x)) continue;
+                for (int i = 0; i < 2 * x.nt; ++i, ++t) {
+                    const int j = i < x.nt ? i : i - x.nt;
+                    int k0, n;
+                    x.tile(j, k0, n);
+                    if (!(ok = atc::wait(v_empty, (t & 1) ^ 1, abort_flag))) break;
+                    atc::expect_tx(v_full, L::TILE);
+                    load_keys<D>(smem + L::OFF_V, vmap, x, j, k0, p.cu_q ? 0 : x.b, v_full);
+                }
             }
+            if (!ok) fail();
+            if (t > 0) tc::mbar_wait_bounded(v_full, (t - 1) & 1, ATC_WAIT);
         } else if (warp == 9) {
             // ----------------------------------------------- S and dP issuer
             const bool leader = elect_one();
@@ -207,7 +216,6 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                         const int off = ((c / 4) * (128 * 128) + (c % 4) * 32) >> 4;
                         tc::mma_bf16(tmem + DQT_S + sl * 128, a + off, b + off, id, c > 0 ? 1u : 0u);
                     }
-                    tc::mma_commit(s_full + sl);
                 }
                 if (!(ok = wait_warp(v_full, t & 1, abort_flag) && wait_warp(dp_free, (t & 1) ^ 1, abort_flag))) break;
                 tc::fence_after_sync();
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                         const int off = ((c / 4) * (128 * 128) + (c % 4) * 32) >> 4;
                         tc::mma_bf16(tmem + DQT_DP, a + TSTEP + off, vd + off, id, c > 0 ? 1u : 0u);
                     }
-                    tc::mma_commit(dp_full);
+                    tc::mma_commit(dp_full);          // S and dP
                     tc::mma_commit(v_empty);
                 }
             }
@@ -281,7 +289,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) dst[c] = src[c];
             }
-            atc::arrive(item_empty + (in & 1));
+            arrive_warp(item_empty + (in & 1));
             if (x.nt < 0) break;
             const bool row_ok = tt < x.nq[0] && hh < (x.heads >> 20);
             const int row_at = row_ok ? tt * p.Hq + hh : -1;
@@ -297,6 +305,8 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                 nl = -kLog2e * __ldg(p.lse_in + b * p.lse_s[0] + tok * p.lse_s[1] + ((x.heads & 0xfffff) + hh) * p.lse_s[2]);
             }
             uint64_t dsum[2] = {0ull, 0ull};
+            const int n_sink = x.sinks & 0xfffffff, head = (x.sinks >> 28) * SF_HEAD;
+            const int base = x.band_lo - (head ? head : n_sink * SF_KT);
             for (int i = 0; i < 2 * x.nt; ++i, ++t) {
                 const bool sum = i < x.nt;
                 const int j = sum ? i : i - x.nt;
@@ -309,13 +319,10 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                     Dr = xd[r] + xd[128 + r];
                     if (w == 0 && row_ok) p.stat[row0 + row_at] = make_float2(-nl, Dr);
                 }
-                const bool sink = j < x.n_sink;
-                const int k0 = sink ? j * SF_KT : x.band_lo + (j - x.n_sink) * SF_KT;
-                const int n = min(SF_KT, (sink ? x.s_end : x.band_hi) - k0), sb = t & 1;
-                if (!wait_warp(s_full + sb, (t >> 1) & 1, abort_flag) || !wait_warp(dp_full, t & 1, abort_flag)) {
-                    ok = false;
-                    break;
-                }
+                const bool apart = head == 0 && j < n_sink;
+                const int k0 = (apart ? 0 : base) + j * SF_KT, sh = j == 0 ? head : 0;
+                const int n = min(SF_KT, (apart ? x.s_end : x.band_hi) - k0), sb = t & 1;
+                if (!wait_warp(dp_full, t & 1, abort_flag)) { ok = false; break; }
                 tc::fence_after_sync();
                 uint32_t s[64], dp[64];
                 const uint32_t tS = lrow + DQT_S + sb * 128 + w * 64, tP = lrow + DQT_DP + w * 64;
@@ -328,16 +335,17 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                     }
                 tc::tmem_ld_wait();
                 tc::fence_before_sync();
-                atc::arrive(dp_free);
+                arrive_warp(dp_free);
                 if (sum) {
-                    atc::arrive(ds_full + sb);            // S has been read
-                } else if (n & 15) {
-                    // rows n .. of the last 16 keys hold whatever lies behind: 0 * inf must not reach dq
+                    arrive_warp(ds_full + sb);            // S has been read
+                } else if ((n & 15) || sh > x.s_end) {
+                    // rows n .. of the last 16 keys, and those between the sinks and the band, hold whatever lies
+                    // there: 0 * inf must not reach dq
                     constexpr int U = D / 8;
-                    const int n16 = (n + 15) & ~15;
+                    const int gap = max(0, sh - x.s_end), rows = gap + ((n + 15) & ~15) - n;
 #pragma unroll 1
-                    for (int u = tid; u < (n16 - n) * U; u += 256) {
-                        const int key = n + u / U, c = u % U;
+                    for (int u = tid; u < rows * U; u += 256) {
+                        const int e = u / U, key = e < gap ? x.s_end + e : n + e - gap, c = u % U;
                         *reinterpret_cast<uint4 *>(smem + L::OFF_K + sb * L::TILE + (c / 8) * (128 * 128) + key * 128 +
                                                    (((c & 7) ^ (key & 7)) * 16)) = make_uint4(0u, 0u, 0u, 0u);
                     }
@@ -349,10 +357,11 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                     if (c0 + c < n) {
                         uint32_t pk[16];
                         const int k = k0 + c0 + c;
-                        const bool whole = c0 + c + 32 <= n && ((k >= lo && k + 32 <= hi) || k + 32 <= s1);
+                        const bool whole = c0 + c + 32 <= n && ((k >= lo && k + 32 <= hi) || k + 32 <= s1) && c0 + c >= sh;
                         uint32_t vis = 0xffffffffu;
                         if (!__all_sync(0xffffffffu, whole))
-                            vis = (bit_range(lo - k, hi - k) | bit_range(0, s1 - k)) & bit_range(0, n - c0 - c);
+                            vis = (bit_range(lo - k, hi - k) | bit_range(sh - c0 - c, s1 - k) |
+                                   bit_range(-c0 - c, (sh ? min(s1, x.s_end) : 0) - c0 - c)) & bit_range(0, n - c0 - c);
                         const bool all = __all_sync(0xffffffffu, vis == 0xffffffffu);
                         if (sum) {
 #pragma unroll
@@ -393,7 +402,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                 if (!sum) {
                     atc::tmem_st_wait();
                     tc::fence_before_sync();
-                    atc::arrive(ds_full + sb);
+                    arrive_warp(ds_full + sb);
                 }
             }
             if (!ok) break;
@@ -441,7 +450,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                 if (to >= 0) *reinterpret_cast<uint4 *>(out0 + (long long)to * D + u * 8) = v;
             }
             tc::fence_proxy_async_smem();
-            atc::arrive(q_empty + (qn & 1));
+            arrive_warp(q_empty + (qn & 1));
             ++qn;
         }
         if (!ok) fail();
@@ -595,11 +604,11 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         tc::mbar_init(kv_full, 1); tc::mbar_init(kv_empty, 1);
         for (int i = 0; i < KVT_STAGES; ++i) { tc::mbar_init(q_full + i, 1); tc::mbar_init(q_empty + i, 1); }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(sd_full + i, 1); tc::mbar_init(pd_full + i, 128); tc::mbar_init(pd_done + i, 1);
+            tc::mbar_init(sd_full + i, 1); tc::mbar_init(pd_full + i, 4); tc::mbar_init(pd_done + i, 1);
             tc::mbar_init(drain + i, 1);
-            tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 256);
+            tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 8);
         }
-        tc::mbar_init(acc_full, 1); tc::mbar_init(acc_free, 256);
+        tc::mbar_init(acc_full, 1); tc::mbar_init(acc_free, 8);
         *abort_flag = 0;
         tc::mbar_fence_init();
     }
@@ -792,7 +801,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 3; ++c) dst[c] = src[c];
             }
-            atc::arrive(item_empty + (in & 1));
+            arrive_warp(item_empty + (in & 1));
             if (x.units < 0) break;
             const bool key_ok = r < x.n_keys;
             // queries that see this key
@@ -867,7 +876,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                 }
                 atc::tmem_st_wait();
                 tc::fence_before_sync();
-                atc::arrive(pd_full + g);
+                arrive_warp(pd_full + g);
             }
             if (!ok) break;
             u0 += x.units;
@@ -925,7 +934,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
             }
             if (x.units > 0) {
                 tc::fence_before_sync();
-                atc::arrive(acc_free);
+                arrive_warp(acc_free);
             }
         }
         if (!ok) fail();

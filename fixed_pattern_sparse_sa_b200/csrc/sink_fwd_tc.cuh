@@ -17,8 +17,10 @@
 // tile's scores are turned into weights the other's products run.  Each row
 // tile's queue is S(0), then P.V(j), S(j+1), ..., across items.
 // A tile of n < 128 keys costs N = n (rounded up to 16) columns in the first
-// product and n rows in the second, so short sinks and window ends are cheap;
-// a row tile skips key tiles that none of its rows sees.
+// product and n rows in the second, but the softmax warps' way around a tile
+// costs much the same: up to 16 sinks therefore share their tile with the
+// first 112 keys of the band.  A row tile skips key
+// tiles that none of its rows sees.
 //
 // Rows of V that not every row of the item sees are cleaned in shared memory
 // first: 0 * inf would put NaN into rows that must not see them.  What is not
@@ -43,6 +45,7 @@ constexpr uint32_t SF_TM_S = 0;          // S / P of A, B: 128 columns each
 constexpr uint32_t SF_TM_O = 256;        // O of A, B: 128 columns each
 constexpr uint32_t SF_TM_COLS = 512;
 constexpr float SF_RAISE = 8.f;
+constexpr int SF_HEAD = 16;              // sinks up to here share their tile with the band
 
 template <int D>
 struct SfSmem {
@@ -71,18 +74,18 @@ struct SinkItem {
     SinkSeq s;
     int b, hk, h0, nh;       // h0: first head, nh: heads of the tile that belong to the group
     int t0, nq_i[2];         // first query; queries of A and B
-    int band_lo, band_hi, s_end, n_sink, nt;
+    int band_lo, band_hi, s_end, nt;
+    int n_sink;              // tiles that hold sinks; every row tile uses them
+    int head;                // SF_HEAD: the sinks take these rows of a tile that they share with the band; 0: they
+                             // have tiles of their own
+    int base;                // tile j >= n_sink (and the shared one) starts at key base + 128 j
     int ja[2], jb[2];        // key tiles that A and B use: the sinks' and [ja, jb) (none: nq_i = 0)
     int clean_lo, clean_hi;  // keys of [band_lo, clean_lo) and [clean_hi, band_hi) are not seen by every row
 
     __device__ __forceinline__ void tile(int j, int &k0, int &n) const {
-        if (j < n_sink) {
-            k0 = j * SF_KT;
-            n = min(SF_KT, s_end - k0);
-        } else {
-            k0 = band_lo + (j - n_sink) * SF_KT;
-            n = min(SF_KT, band_hi - k0);
-        }
+        const bool apart = j < n_sink && head == 0;
+        k0 = (apart ? 0 : base) + j * SF_KT;
+        n = min(SF_KT, (apart ? s_end : band_hi) - k0);
     }
     __device__ __forceinline__ bool active(int i, int j) const {
         return (i ? nq_i[1] : nq_i[0]) > 0 && (j < n_sink || (j >= (i ? ja[1] : ja[0]) && j < (i ? jb[1] : jb[0])));
@@ -143,12 +146,14 @@ __device__ __forceinline__ bool sink_item(const SinkParams &p, const SinkTiles &
         x.clean_lo = lo;
     }
     x.n_sink = (x.s_end + SF_KT - 1) / SF_KT;
-    x.nt = x.n_sink + (x.band_hi - x.band_lo + SF_KT - 1) / SF_KT;
+    x.head = x.s_end > 0 && x.s_end <= SF_HEAD && x.band_hi > x.band_lo ? SF_HEAD : 0;
+    x.base = x.band_lo - (x.head ? x.head : x.n_sink * SF_KT);
+    x.nt = x.band_hi > x.band_lo ? (x.band_hi - x.base + SF_KT - 1) / SF_KT : x.n_sink;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         // a row that still sees sinks inside the band needs the band from its start
-        x.ja[i] = x.n_sink + (s1_max[i] > x.band_lo ? 0 : max(0, lo_min[i] - x.band_lo) / SF_KT);
-        x.jb[i] = x.n_sink + max(0, hi_max[i] - x.band_lo + SF_KT - 1) / SF_KT;
+        x.ja[i] = max(x.n_sink, s1_max[i] > x.band_lo ? 0 : (lo_min[i] - x.base) / SF_KT);
+        x.jb[i] = hi_max[i] > x.band_lo ? (hi_max[i] - x.base + SF_KT - 1) / SF_KT : 0;
     }
     return true;
 }
@@ -172,6 +177,24 @@ __device__ __forceinline__ void load_4d(void *dst, const CUtensorMap *map, int x
         " [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(tc::smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(tc::smem_u32(bar))
         : "memory");
+}
+// Maps of K or V: boxes of 128 rows, of SF_HEAD and of the rest.
+struct KeyMaps { CUtensorMap all, head, rest; };
+// Key tile j of item x (K or V: 128 rows) into dst.
+template <int D>
+__device__ __forceinline__ void load_keys(unsigned char *dst, const KeyMaps &m, const SinkItem &x, int j, int k0, int batch,
+                                          uint64_t *bar) {
+    const int row = (int)x.s.k0;
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) {
+        unsigned char *to = dst + h * (SF_KT * 128);
+        if (j > 0 || x.head == 0) {
+            load_4d(to, &m.all, h * 64, x.hk, row + k0, batch, bar);
+        } else {
+            load_4d(to, &m.head, h * 64, x.hk, row, batch, bar);
+            load_4d(to + SF_HEAD * 128, &m.rest, h * 64, x.hk, row + k0 + SF_HEAD, batch, bar);
+        }
+    }
 }
 // kind::f16 instruction descriptor operand format of T
 template <typename T>
@@ -221,6 +244,11 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
     return __all_sync(0xffffffffu, atc::wait(bar, parity, abort_flag)) != 0;
 }
+// one arrival for a warp, after all its lanes
+__device__ __forceinline__ void arrive_warp(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) atc::arrive(bar);
+}
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
 template <int N>
@@ -237,7 +265,8 @@ struct alignas(16) SfItem {
     int nt;                  // key tiles; -1 ends the stream
     int nq[2];               // queries of A and B
     int pos;                 // position of the first query
-    int band_lo, band_hi, s_end, n_sink;
+    int band_lo, band_hi, s_end;
+    int sinks;               // head / SF_HEAD << 28 | n_sink
     int ja[2], jb[2];
     int clean_lo, clean_hi;
     int heads;               // first head | heads of the tile << 20
@@ -249,8 +278,8 @@ enum : uint32_t { TI_STEPS = 15u, TI_A = 16u, TI_B = 32u, TI_FIRST = 64u, TI_LAS
 
 template <typename T, int D>
 __global__ void __launch_bounds__(SF_THREADS, 1)
-    sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                       const __grid_constant__ CUtensorMap vmap, const __grid_constant__ SinkParams p,
+    sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ KeyMaps kmap,
+                       const __grid_constant__ KeyMaps vmap, const __grid_constant__ SinkParams p,
                        const __grid_constant__ SinkTiles tl) {
     grid_dependency_sync();
     using L = SfSmem<D>;
@@ -275,9 +304,9 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(q_full + i, 1); tc::mbar_init(q_empty + i, 1);
             tc::mbar_init(s_full + i, 1); tc::mbar_init(o_full + i, 1);
-            tc::mbar_init(p_full + 2 * i, 128); tc::mbar_init(p_full + 2 * i + 1, 128);
+            tc::mbar_init(p_full + 2 * i, 4); tc::mbar_init(p_full + 2 * i + 1, 4);
             tc::mbar_init(drain + i, 1);
-            tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 256);
+            tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 8);
         }
         for (int i = 0; i < SF_SLOTS; ++i) { tc::mbar_init(kv_full + i, 1); tc::mbar_init(kv_empty + i, 2); }
         *abort_flag = 0;
@@ -408,7 +437,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                 SinkItem x;
                 if (!sink_item<2>(p, tl, it, x)) continue;
                 ok = hand_over(SfItem{x.nt, {x.nq_i[0], x.nq_i[1]}, (int)x.s.pos0 + x.t0, x.band_lo, x.band_hi, x.s_end,
-                                      x.n_sink, {x.ja[0], x.ja[1]}, {x.jb[0], x.jb[1]}, x.clean_lo, x.clean_hi,
+                                      x.n_sink | x.head / SF_HEAD << 28, {x.ja[0], x.ja[1]}, {x.jb[0], x.jb[1]}, x.clean_lo, x.clean_hi,
                                       x.h0 | x.nh << 20,
                                       (int)((p.cu_q ? 0 : x.b * p.Tq) + x.s.q0) + x.t0});
                 if (!ok) break;
@@ -434,9 +463,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                                              (x.active(1, j) ? TI_B : 0u) | (j == 0 ? TI_FIRST : 0u) |
                                              (j + 1 == x.nt ? TI_LAST : 0u) | TI_TILE;
                         atc::expect_tx(kv_full + sl, L::TILE);
-                        for (int h = 0; h < HALVES; ++h)
-                            load_4d(smem + L::OFF_KV + sl * L::TILE + h * (SF_KT * 128), v ? &vmap : &kmap, h * 64,
-                                    x.hk, (int)(x.s.k0 + k0), qb, kv_full + sl);
+                        load_keys<D>(smem + L::OFF_KV + sl * L::TILE, v ? vmap : kmap, x, j, k0, qb, kv_full + sl);
                         if (j == 0 && v == 0) ok = load_q(0) && load_q(1);
                     }
                 }
@@ -485,7 +512,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) dst[c] = src[c];
             }
-            atc::arrive(item_empty + (in & 1));
+            arrive_warp(item_empty + (in & 1));
             if (x.nt < 0) break;
             const int nqi = i ? x.nq[1] : x.nq[0], ja = i ? x.ja[1] : x.ja[0], jb = i ? x.jb[1] : x.jb[0];
             const bool row_ok = tt < nqi && hh < (x.heads >> 20);
@@ -499,36 +526,40 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
             float m = -INFINITY, l = 0.f;
             bool first = true;
             // the sinks' tiles, then [ja, jb): next tile j at key k0, the range's end, the range to clean
-            bool in_sink = x.n_sink > 0;
-            int j = in_sink ? 0 : ja, jend = nqi == 0 ? 0 : in_sink ? x.n_sink : jb;
-            int k0 = in_sink ? 0 : x.band_lo + (ja - x.n_sink) * SF_KT, kend = in_sink ? x.s_end : x.band_hi;
-            int cl = in_sink ? 0 : x.clean_lo, ch = in_sink ? x.s_end : x.clean_hi;
+            const int n_sink = x.sinks & 0xfffffff, head = (x.sinks >> 28) * SF_HEAD;
+            const int base = x.band_lo - (head ? head : n_sink * SF_KT);
+            bool in_sink = n_sink > 0;
+            int j = in_sink ? 0 : ja, jend = in_sink ? n_sink : jb;
+            const bool apart = in_sink && head == 0;
+            int k0 = (apart ? 0 : base) + j * SF_KT, kend = apart ? x.s_end : x.band_hi;
+            int cl = apart ? 0 : x.clean_lo, ch = apart ? x.s_end : x.clean_hi;
             if (nqi > 0) for (;; ++j, k0 += SF_KT) {
                 if (j >= jend) {
                     if (!in_sink || ja >= jb) break;
                     in_sink = false;
-                    j = ja; jend = jb; k0 = x.band_lo + (ja - x.n_sink) * SF_KT; kend = x.band_hi;
+                    j = ja; jend = jb; k0 = base + ja * SF_KT; kend = x.band_hi;
                     cl = x.clean_lo; ch = x.clean_hi;
                 }
                 const int n = min(SF_KT, kend - k0), n16 = (n + 15) & ~15;
-                // the first row tile that uses this V tile cleans the rows that not every row sees
-                if ((k0 < cl || k0 + n16 > ch) &&
-                    (i == 0 || !(x.nq[0] > 0 && (in_sink || (j >= x.ja[0] && j < x.jb[0]))))) {
+                const int sh = in_sink ? head : 0;         // rows of the tile that the sinks share
+                // clean the rows of V that not every row of the item sees.  Both row tiles do, each before its own
+                // P: their products are issued by different warps, and cleaning twice changes nothing
+                if (k0 + sh < cl || k0 + n16 > ch || sh > x.s_end) {
                     const uint32_t kt = kt0 + j;
                     const int sl = 2 * (kt & 1) + 1, ca = min(n, max(0, cl - k0)), cb = min(n, max(0, ch - k0));
                     if (!wait_warp(kv_full + sl, (kt >> 1) & 1, abort_flag)) { ok = false; break; }
                     // 16-byte units of the rows [0, ca) and [cb, n16)
                     constexpr int U = D / 8;
                     const int gap = max(cb, ca) - ca, rows = n16 - gap;
-                    bool found = false;
 #pragma unroll 1
                     for (int u = r; u < rows * U; u += 128) {
                         int key = u / U;
                         const int c = u % U;
                         if (key >= ca) key += gap;
+                        if (key < sh && key < x.s_end) continue;
                         uint4 *at = reinterpret_cast<uint4 *>(smem + L::OFF_KV + sl * L::TILE + (c / 8) * (SF_KT * 128) +
                                                               key * 128 + (((c & 7) ^ (key & 7)) * 16));
-                        if (key >= n) {
+                        if (key >= n || key < sh) {
                             *at = make_uint4(0u, 0u, 0u, 0u);
                             continue;
                         }
@@ -541,11 +572,11 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                             if (not_finite16<T>(w[e] >> 16)) { w[e] &= 0xffffu; bad = true; }
                         }
                         if (bad) {
+                            *dirty = 1;               // first: the other row tile may find the unit clean
+                            __threadfence_block();
                             *at = make_uint4(w[0], w[1], w[2], w[3]);
-                            found = true;
                         }
                     }
-                    if (found) *dirty = 1;
                     tc::fence_proxy_async_smem();
                 }
                 // S of this tile; P.V of the tile before it was issued earlier and is done with it
@@ -564,7 +595,9 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                         mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(s[c + e]),
                                                 __uint_as_float(s[c + e + 1]));
                 };
-                const bool whole = n == SF_KT && ((k0 >= lo && k0 + n <= hi) || k0 + n <= s1);
+                // sinks: the columns [sh, v1), and of a shared tile [0, sees)
+                const int v1 = s1 - k0, sees = sh ? min(s1, x.s_end) : 0;
+                const bool whole = n == SF_KT && ((k0 >= lo && k0 + n <= hi) || k0 + n <= s1) && sh == 0;
                 if (__all_sync(0xffffffffu, whole)) {
 #pragma unroll
                     for (int c = 0; c < SF_KT; c += 32) chunk_max(c);
@@ -573,7 +606,8 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                     for (int c = 0; c < SF_KT; c += 32)
                         if (c < n) {
                             const int k = k0 + c;
-                            const uint32_t vis = (bit_range(lo - k, hi - k) | bit_range(0, s1 - k)) & bit_range(0, n - c);
+                            const uint32_t vis = (bit_range(lo - k, hi - k) | bit_range(sh - c, v1 - c) | bit_range(-c, sees - c)) &
+                                                 bit_range(0, n - c);
                             if (__any_sync(0xffffffffu, vis != 0xffffffffu)) {
 #pragma unroll
                                 for (int e = 0; e < 32; ++e)
@@ -624,7 +658,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                     if (c == 32 || c == 96) {         // a half of P is in place
                         atc::tmem_st_wait();
                         tc::fence_before_sync();
-                        atc::arrive(p_full + 2 * i + c / 64);
+                        arrive_warp(p_full + 2 * i + c / 64);
                     }
                 }
                 float r0, r1;
