@@ -14,8 +14,10 @@
 // rounded to the inputs' type (half a step a weight, as the output is).
 //
 // The tensor cores and the softmax alternate between A and B: while one
-// tile's scores are turned into weights the other's products run.  Each row
-// tile's queue is S(0), then P.V(j), S(j+1), ..., across items.
+// tile's scores are turned into weights the other's products run.  S and P of
+// a row tile are held in two halves of 64 keys: while the softmax warps work on
+// one, the product of the other and its next S run.  Each row tile's queue is
+// S(0), S(1), then P.V(u), S(u + 2), ... over the halves u, across items.
 // A tile of n < 128 keys costs N = n (rounded up to 16) columns in the first
 // product and n rows in the second, but the softmax warps' way around a tile
 // costs much the same: up to 16 sinks therefore share their tile with the
@@ -54,9 +56,9 @@ struct SfSmem {
     static constexpr int OFF_KV = OFF_Q + 2 * TILE;
     static constexpr int OFF_STAGE = OFF_KV + SF_SLOTS * TILE;      // outputs: 32 rows x 128 B per softmax warp
     static constexpr int OFF_BAR = OFF_STAGE + 8 * 4096;
-    // q_full[2], q_empty[2], kv_full[S], kv_empty[S], s_full[2], p_full[2][2], o_full[2], drain[2],
-    // item_full[2], item_empty[2]
-    static constexpr int N_BAR = 4 + 2 * SF_SLOTS + 8 + 2 + 4;
+    // q_full[2], q_empty[2], kv_full[S], kv_empty[S], s_full[2][2], p_full[2][2], pv_done[2][2],
+    // o_full[2], drain[2], item_full[2], item_empty[2]
+    static constexpr int N_BAR = 4 + 2 * SF_SLOTS + 12 + 4 + 4;
     static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;   // tmem slot, abort flag, dirty flag, tile info[2]
     static constexpr int OFF_ITEM = OFF_MISC + 32;         // two work items of the softmax warps
     static constexpr int TOTAL = OFF_ITEM + 2 * 64;
@@ -288,7 +290,8 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
     unsigned char *smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
     uint64_t *q_full = bars, *q_empty = bars + 2, *kv_full = bars + 4, *kv_empty = kv_full + SF_SLOTS;
-    uint64_t *s_full = kv_empty + SF_SLOTS, *p_full = s_full + 2, *o_full = p_full + 4, *drain = o_full + 2;
+    uint64_t *s_full = kv_empty + SF_SLOTS, *p_full = s_full + 4, *pv_done = p_full + 4, *o_full = pv_done + 4;
+    uint64_t *drain = o_full + 2;
     uint64_t *item_full = drain + 2, *item_empty = item_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
@@ -303,8 +306,11 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(q_full + i, 1); tc::mbar_init(q_empty + i, 1);
-            tc::mbar_init(s_full + i, 1); tc::mbar_init(o_full + i, 1);
-            tc::mbar_init(p_full + 2 * i, 4); tc::mbar_init(p_full + 2 * i + 1, 4);
+            tc::mbar_init(o_full + i, 1);
+            for (int h = 0; h < 2; ++h) {
+                tc::mbar_init(s_full + 2 * i + h, 1); tc::mbar_init(p_full + 2 * i + h, 4);
+                tc::mbar_init(pv_done + 2 * i + h, 1);
+            }
             tc::mbar_init(drain + i, 1);
             tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 8);
         }
@@ -341,23 +347,21 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
         const uint64_t vd = atc::desc_sw128(tc::smem_u32(smem + L::OFF_KV), SF_KT * 128, 1024);
         const uint32_t tS = tmem + SF_TM_S + I * 128, tO = tmem + SF_TM_O + I * 128;
         bool ok = true;
-        uint32_t qpar = 1, ppar = 0;                  // parities of the current item's Q, of P
+        uint32_t qpar = 1;                            // parity of the current item's Q
+        uint32_t ppar = 0;                            // parities of P's halves in bits 0, 1
         uint32_t begun = 0;                           // O holds a product of the current item
-        // S over the key tile in K slot k
-        auto issue_s = [&](uint32_t info, int k) {
-            if (leader) {
-                if (info & USES) {
-                    const uint32_t id = tc::make_idesc(1, F, 128, 0) | ((info & TI_STEPS) << 18);   // N / 8 at bit 17
-                    const uint64_t b = kd + k * TSTEP;
+        // S over half h of the key tile in K slot k
+        auto issue_s = [&](uint32_t info, int k, int h) {
+            const int steps = (int)(info & TI_STEPS) - 4 * h;      // 16-key steps of this half
+            if ((info & USES) && steps > 0 && leader) {
+                const uint32_t id = tc::make_idesc(1, F, 128, 0) | ((uint32_t)min(steps, 4) << 18);   // N / 8 at bit 17
+                const uint64_t b = kd + k * TSTEP + h * (64 * 128 >> 4);
 #pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                        const int off = ((c / 4) * (128 * 128) + (c % 4) * 32) >> 4;
-                        tc::mma_bf16(tS, qd + off, b + off, id, c > 0 ? 1u : 0u);
-                    }
-                    tc::mma_commit(s_full + I);
+                for (int c = 0; c < D / 16; ++c) {
+                    const int off = ((c / 4) * (128 * 128) + (c % 4) * 32) >> 4;
+                    tc::mma_bf16(tS + h * 64, qd + off, b + off, id, c > 0 ? 1u : 0u);
                 }
-                if (info & TI_LAST) tc::mma_commit(q_empty + I);
-                if (info & TI_TILE) tc::mma_commit(kv_empty + k);
+                tc::mma_commit(s_full + 2 * I + h);
             }
         };
         ok = wait_warp(kv_full + 0, 0, abort_flag);
@@ -367,7 +371,12 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
             ok = wait_warp(q_full + I, qpar, abort_flag);
             if (ok) {
                 tc::fence_after_sync();
-                issue_s(info, 0);
+                issue_s(info, 0, 0);
+                issue_s(info, 0, 1);
+                if (leader) {
+                    tc::mma_commit(kv_empty + 0);
+                    if (info & TI_LAST) tc::mma_commit(q_empty + I);
+                }
             }
         }
         uint32_t t = 0;                               // key tile; K of tile t in slot 2 (t & 1), V in the next
@@ -381,30 +390,35 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                 qpar ^= 1;
                 if (!(ok = wait_warp(q_full + I, qpar, abort_flag))) break;
             }
-            if (info & USES) {
-                // P.V in two halves, so the first runs while the second's weights are computed; the
-                // softmax warps write an item's first P after they have read the O of the item before
-                const uint64_t v = vd + vs * TSTEP;
-                const int steps = info & TI_STEPS;
+            const uint64_t v = vd + vs * TSTEP;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!(ok = wait_warp(p_full + 2 * I + h, ppar, abort_flag))) break;
+            for (int h = 0; h < 2; ++h) {
+                const int steps = (int)(info & TI_STEPS) - 4 * h;
+                if ((info & USES) && steps > 0) {
+                    // the softmax warps write an item's first P after they have read the O of the item before
+                    if (!(ok = wait_warp(p_full + 2 * I + h, (ppar >> h) & 1, abort_flag))) break;
                     tc::fence_after_sync();
                     if (leader) {
 #pragma unroll
-                        for (int c = 4 * h; c < 4 * h + 4; ++c)
-                            if (c < steps) tc::mma_bf16_ts(tO, tS + c * 8, v + c * 128, ID_O, c > 0 ? 1u : begun);
+                        for (int c = 0; c < 4; ++c)
+                            if (c < steps)
+                                tc::mma_bf16_ts(tO, tS + h * 64 + c * 8, v + (4 * h + c) * 128, ID_O, c > 0 ? 1u : begun);
+                        tc::mma_commit(pv_done + 2 * I + h);
                     }
+                    ppar ^= 1u << h;
+                    begun = 1;
                 }
-                if (!ok) break;
-                ppar ^= 1;
-                begun = 1;
+                if ((info & TI_LAST) && begun && h == ((info & TI_STEPS) > 4 ? 1 : 0) && leader)
+                    tc::mma_commit(o_full + I);       // the item's last product
+                tc::fence_after_sync();
+                issue_s(next, ks, h);                 // into the half whose P this product has read
             }
+            if (!ok) break;
             if (leader) {
-                if ((info & TI_LAST) && begun) tc::mma_commit(o_full + I);
                 tc::mma_commit(kv_empty + vs);
+                if (next & TI_TILE) tc::mma_commit(kv_empty + ks);
+                if (next & TI_LAST) tc::mma_commit(q_empty + I);
             }
-            issue_s(next, ks);
             if (info & TI_LAST) begun = 0;
             info = next;
             ++t;
@@ -501,7 +515,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
         const int tt = r / tl.HB, hh = r - tt * tl.HB;
         unsigned char *stage = smem + L::OFF_STAGE + warp * 4096;
         bool ok = true;
-        uint32_t spar = 0, opar = 0;                  // parities of s_full, o_full
+        uint32_t spar = 0, opar = 0;                  // parities of S's halves in bits 0, 1; of o_full
         uint32_t kt0 = 0;                             // key tiles of the stream before this item
         for (uint32_t in = 0;; ++in) {
             if (!wait_warp(item_full + (in & 1), (in >> 1) & 1, abort_flag)) { ok = false; break; }
@@ -525,6 +539,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
             }
             float m = -INFINITY, l = 0.f;
             bool first = true;
+            uint32_t used = 0;                        // halves with a product into this item's O
             // the sinks' tiles, then [ja, jb): next tile j at key k0, the range's end, the range to clean
             const int n_sink = x.sinks & 0xfffffff, head = (x.sinks >> 28) * SF_HEAD;
             const int base = x.band_lo - (head ? head : n_sink * SF_KT);
@@ -579,69 +594,70 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                     }
                     tc::fence_proxy_async_smem();
                 }
-                // S of this tile; P.V of the tile before it was issued earlier and is done with it
-                if (!wait_warp(s_full + i, spar, abort_flag)) { ok = false; break; }
-                spar ^= 1;
-                tc::fence_after_sync();
-                uint32_t s[SF_KT];
-#pragma unroll
-                for (int c = 0; c < SF_KT; c += 32)
-                    if (c < n) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(s + c));
-                tc::tmem_ld_wait();
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                auto chunk_max = [&](int c) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(s[c + e]),
-                                                __uint_as_float(s[c + e + 1]));
-                };
                 // sinks: the columns [sh, v1), and of a shared tile [0, sees)
                 const int v1 = s1 - k0, sees = sh ? min(s1, x.s_end) : 0;
-                const bool whole = n == SF_KT && ((k0 >= lo && k0 + n <= hi) || k0 + n <= s1) && sh == 0;
-                if (__all_sync(0xffffffffu, whole)) {
+                const bool row_whole = ((k0 >= lo && k0 + n <= hi) || k0 + n <= s1) && sh == 0;
+                const bool whole = __all_sync(0xffffffffu, row_whole);
+#pragma unroll 1
+                for (int h = 0; h * 64 < n; ++h) {
+                    // S of this half; the other half's was issued before, its P.V may still run
+                    if (!wait_warp(s_full + 2 * i + h, (spar >> h) & 1, abort_flag)) { ok = false; break; }
+                    tc::fence_after_sync();
+                    const int c0 = h * 64, nh = n - c0;
+                    uint32_t s[64];
+                    tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(s));
+                    tmem_ld32(tS + c0 + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+                    tc::tmem_ld_wait();
+                    if (!whole || nh < 64) {
 #pragma unroll
-                    for (int c = 0; c < SF_KT; c += 32) chunk_max(c);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < SF_KT; c += 32)
-                        if (c < n) {
-                            const int k = k0 + c;
-                            const uint32_t vis = (bit_range(lo - k, hi - k) | bit_range(sh - c, v1 - c) | bit_range(-c, sees - c)) &
-                                                 bit_range(0, n - c);
+                        for (int c = 0; c < 64; c += 32) {
+                            const int q = c0 + c;
+                            const uint32_t vis = (bit_range(lo - k0 - q, hi - k0 - q) | bit_range(sh - q, v1 - q) |
+                                                  bit_range(-q, sees - q)) & bit_range(0, n - q);
                             if (__any_sync(0xffffffffu, vis != 0xffffffffu)) {
 #pragma unroll
                                 for (int e = 0; e < 32; ++e)
                                     if (!((vis >> e) & 1u)) s[c + e] = __float_as_uint(-INFINITY);
                             }
-                            chunk_max(c);
                         }
-                }
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-                const bool raise = mt > m + (m == -INFINITY ? 0.f : SF_RAISE);
-                float alpha = 1.f;
-                if (raise) {
-                    alpha = m == -INFINITY ? 0.f : ex2_fast(m - mt);
-                    m = mt;
-                    l *= alpha;
-                }
-                if (!first && __any_sync(0xffffffffu, raise)) {
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t o16[16];
-                        tc::tmem_ld16(tO + c, o16);
-                        tc::tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o16[e] = __float_as_uint(__uint_as_float(o16[e]) * alpha);
-                        atc::tmem_st16(tO + c, o16);
                     }
-                }
-                first = false;
-                const float nb = m == -INFINITY ? 0.f : -m;
-                const uint64_t nb2 = f2_pack(nb, nb), sc2 = f2_pack(p.scale_log2, p.scale_log2);
-                uint64_t rs[2] = {0ull, 0ull};
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < SF_KT; c += 32) {
-                    if (c < n) {
+                    for (int e = 0; e < 64; e += 2)
+                        mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                    const bool raise = mt > m + (m == -INFINITY ? 0.f : SF_RAISE);
+                    float alpha = 1.f;
+                    if (raise) {
+                        alpha = m == -INFINITY ? 0.f : ex2_fast(m - mt);
+                        m = mt;
+                        l *= alpha;
+                    }
+                    if (!first && __any_sync(0xffffffffu, raise)) {
+                        // every product into O so far: the last one of each half (one of them is older and done)
+                        bool got = true;
+                        if (used & 1u) got = wait_warp(pv_done + 2 * i, ((spar & 1) ^ 1), abort_flag);
+                        if (used & 2u) got = wait_warp(pv_done + 2 * i + 1, ((spar >> 1) & 1) ^ 1, abort_flag) && got;
+                        if (!got) { ok = false; break; }
+                        tc::fence_after_sync();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o16[16];
+                            tc::tmem_ld16(tO + c, o16);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o16[e] = __float_as_uint(__uint_as_float(o16[e]) * alpha);
+                            atc::tmem_st16(tO + c, o16);
+                        }
+                    }
+                    first = false;
+                    used |= 1u << h;
+                    spar ^= 1u << h;
+                    const float nb = m == -INFINITY ? 0.f : -m;
+                    const uint64_t nb2 = f2_pack(nb, nb), sc2 = f2_pack(p.scale_log2, p.scale_log2);
+                    uint64_t rs[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
@@ -653,17 +669,16 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                             rs[(e >> 1) & 1] = f2_add(rs[(e >> 1) & 1], f2_pack(p0, p1));
                             pk[e / 2] = pack2<T>(p0, p1);
                         }
-                        atc::tmem_st16(tS + c / 2, pk);
+                        atc::tmem_st16(tS + c0 + c / 2, pk);
                     }
-                    if (c == 32 || c == 96) {         // a half of P is in place
-                        atc::tmem_st_wait();
-                        tc::fence_before_sync();
-                        arrive_warp(p_full + 2 * i + c / 64);
-                    }
+                    float r0, r1;
+                    f2_unpack(f2_add(rs[0], rs[1]), r0, r1);
+                    l += r0 + r1;
+                    atc::tmem_st_wait();
+                    tc::fence_before_sync();
+                    arrive_warp(p_full + 2 * i + h);
                 }
-                float r0, r1;
-                f2_unpack(f2_add(rs[0], rs[1]), r0, r1);
-                l += r0 + r1;
+                if (!ok) break;
             }
             if (!ok) break;
             kt0 += x.nt;
