@@ -18,8 +18,9 @@
 // one item merges its warps in shared memory; what remains spans several
 // warps or CTAs and is joined by paged_join_kernel from fp32 partials.
 //
-// P is rounded to the caches' type for the second product (an error of half
-// a step per weight, below the rounding of the output); all sums are fp32.
+// P enters the second product as two values of the caches' type, its rounding
+// and what that leaves (16 to 22 bits), so that a row of few keys is as exact
+// as its output's type; the bytes bind, not the products.  All sums are fp32.
 #pragma once
 
 #include "sa_common.cuh"
@@ -27,9 +28,9 @@
 
 namespace sa {
 
-constexpr int PD_NW = 8;                  // warps per CTA
+constexpr int PD_NW = 12;                 // warps per CTA
 constexpr int PD_NK = 16;                 // keys per chunk
-constexpr int PD_STAGES = 3;              // chunks in flight per warp
+constexpr int PD_STAGES = 2;              // ring stages per warp: one chunk in flight, one in use
 constexpr int PD_THREADS = PD_NW * 32;
 constexpr int PD_MIN_CHUNKS = 2;          // chunks per warp below which fewer CTAs share the list
 constexpr float PD_RAISE = 8.f;           // log2 headroom before the accumulators are rescaled
@@ -42,6 +43,7 @@ struct PdSmem {
     static constexpr int OFF_ML = PD_NW * RING;               // [NW][16] m, [NW][16] l
     static constexpr int OFF_SCAN = OFF_ML + PD_NW * 32 * 4;
     static constexpr int TOTAL = OFF_SCAN + 256;
+    static_assert((2 * 8 + 4) * PD_NW <= 256, "scan area");
     static_assert(RING >= 16 * D * 4, "a warp's ring holds its fp32 accumulators at the merge");
 };
 
@@ -373,8 +375,16 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const PagedPar
                     s[t][e] = ex2_fast(s[t][e] - mb[e >> 1]);
                     l[e >> 1] += s[t][e];
                 }
-            unsigned pa[4] = {pack2<T>(s[0][0], s[0][1]), pack2<T>(s[0][2], s[0][3]), pack2<T>(s[1][0], s[1][1]),
-                              pack2<T>(s[1][2], s[1][3])};
+            unsigned pa[4], pb[4];                // P = pa + pb
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float x = s[t][2 * e], y = s[t][2 * e + 1];
+                    const T xh = from_f<T>(x), yh = from_f<T>(y);
+                    pa[2 * t + e] = pack2<T>(x, y);
+                    pb[2 * t + e] = pack2<T>(x - to_f(xh), y - to_f(yh));
+                }
             {
                 // V transposed: (keys 0-7, c 0-7), (keys 8-15, c 0-7), (keys 0-7, c 8-15), (keys 8-15, c 8-15)
                 const int r = (lane & 15), ub = lane >> 4;
@@ -385,6 +395,8 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const PagedPar
                     ldsm_x4_ta(b0, b1, b2, b3, row + (((i * 2 + ub) ^ (r & 7)) * 16));
                     mma_16816<T>(o[2 * i], pa, b0, b1);
                     mma_16816<T>(o[2 * i + 1], pa, b2, b3);
+                    mma_16816<T>(o[2 * i], pb, b0, b1);
+                    mma_16816<T>(o[2 * i + 1], pb, b2, b3);
                 }
             }
             __syncwarp();                     // every lane has read the stage before it is loaded again
@@ -429,8 +441,9 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const PagedPar
             *reinterpret_cast<float2 *>(mine + ((lane >> 2) + e * 8) * D + i * 8 + (lane & 3) * 2) =
                 make_float2(o[i][2 * e], o[i][2 * e + 1]);
     __syncthreads();
-    // 16 rows over the threads: thread t holds columns of row t / 16
-    constexpr int TPR = PD_THREADS / 16, CPT = D / TPR;
+    // 16 rows over the first 256 threads
+    if (tid >= 256) return;
+    constexpr int TPR = 16, CPT = D / TPR;
     const int r = tid / TPR, c = (tid % TPR) * CPT;
     float M = -INFINITY, Ls = 0.f, acc[CPT] = {};
     for (int w = 0; w < PD_NW; ++w) M = fmaxf(M, sm[w * 16 + r]);
