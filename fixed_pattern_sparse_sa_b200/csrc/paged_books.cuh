@@ -262,22 +262,26 @@ __global__ void __cluster_dims__(PB_CTAS, 1, 1) __launch_bounds__(PB_THREADS) pa
         }
 }
 
-// One warp per list entry.  A table entry is taken out by an exchange, so a
-// sequence that is listed twice gives each page back once.
+// One thread per table entry of a listed sequence: the exchange and the count
+// are two dependent trips to L2, so they go side by side (a warp per sequence
+// that walked its row took 36 us for 192 rows of 1025 entries).  An entry is
+// taken out by an exchange, so a sequence that is listed twice gives each page
+// back once.
 __global__ void __launch_bounds__(256) paged_free_kernel(const BooksParams p, int window, int sinks) {
     grid_dependency_sync();
-    const int lane = threadIdx.x & 31;
-    for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < p.n; i += gridDim.x * 8) {
+    for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
         const int s = p.a[i];
         if (s < 0 || s >= p.S) {
-            if (lane == 0) raise_error(p.err, ERR_BAD_INDEX);
+            if (blockIdx.y == 0 && threadIdx.x == 0) raise_error(p.err, ERR_BAD_INDEX);
             continue;
         }
         const long long gone = window > 0 ? (long long)p.lens[s] - window : 0;
-        for (int k = lane; k < p.max_pages; k += 32) {
+        for (int k = blockIdx.y * 256 + threadIdx.x; k < p.max_pages; k += gridDim.y * 256) {
             const long long lo = (long long)k * p.page;
             if (window > 0 && (lo < sinks || lo + p.page > gone)) continue;
-            const int id = atomicExch(&p.table[(size_t)s * p.max_pages + k], -1);
+            int *at = &p.table[(size_t)s * p.max_pages + k];
+            if (*at == -1) continue;
+            const int id = atomicExch(at, -1);
             if (id < 0) continue;
             if (id >= p.n_pages) { raise_error(p.err, ERR_BAD_INDEX); continue; }
             if (atomicSub(&p.refcount[id], 1) <= 0) {
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(256) paged_free_kernel(const BooksParams p, in
                 raise_error(p.err, ERR_BAD_INDEX);
             }
         }
-        if (window == 0 && lane == 0) p.lens[s] = 0;
+        if (window == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.lens[s] = 0;
     }
 }
 

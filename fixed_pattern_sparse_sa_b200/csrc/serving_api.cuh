@@ -561,7 +561,7 @@ extern "C" int sa_paged_free(int32_t *block_table, int32_t *seq_lens, int32_t *r
     if (rc) return rc;
     p.table = block_table; p.lens = seq_lens; p.refcount = refcount;
     p.S = S; p.max_pages = max_pages; p.page = page; p.n_pages = n_pages; p.a = seqs; p.n = n;
-    const unsigned grid = (unsigned)std::min((n + 7) / 8, sm_count() * 8);
+    const dim3 grid((unsigned)std::min(n, 1 << 20), (unsigned)std::min(std::max((max_pages + 255) / 256, 1), 64));
     launch_k("paged_free_kernel", paged_free_kernel, grid, 256, 0, as_stream(stream), p, window, sinks);
     SA_CHECK_LAUNCH("paged_free_kernel");
     return SA_OK;
