@@ -15,8 +15,8 @@
 // dq up from the key-major pass would move 4 bytes per element of dq and key
 // tile through L2 atomics instead, in varying order.
 //
-// P and dS are rounded to bf16 for the second products; sums are fp32 and
-// rounded once.
+// P and dS are rounded to bf16 for the second products (with SPLIT what that
+// leaves enters as another product); sums are fp32 and rounded once.
 #pragma once
 
 #include "sink_fwd_tc.cuh"
@@ -60,7 +60,7 @@ struct SqSmem {
     static_assert(8 * 32 * D <= 2 * TILE, "the staged rows fit the item's Q and dO");
 };
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(SB_THREADS, 1)
     sink_dq_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap domap,
                       const __grid_constant__ KeyMaps kmap, const __grid_constant__ KeyMaps vmap,
@@ -260,6 +260,13 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                         if (c < steps)
                             tc::mma_bf16_ts(tmem + DQT_DQ, tmem + DQT_S + sl * 128 + (c / 4) * 64 + (c % 4) * 8, b + c * 128,
                                             ID_Q, c > 0 ? 1u : (info & TI_START ? 0u : 1u));
+                    if constexpr (SPLIT) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            if (c < steps)
+                                tc::mma_bf16_ts(tmem + DQT_DQ, tmem + DQT_S + sl * 128 + (c / 4) * 64 + 32 + (c % 4) * 8,
+                                                b + c * 128, ID_Q, 1u);
+                    }
                     tc::mma_commit(k_empty + sl);
                     if (info & TI_LAST) tc::mma_commit(dq_full);
                 }
@@ -355,7 +362,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 64; c += 32) {
                     if (c0 + c < n) {
-                        uint32_t pk[16];
+                        uint32_t pk[16], pr[16];
                         const int k = k0 + c0 + c;
                         const bool whole = c0 + c + 32 <= n && ((k >= lo && k + 32 <= hi) || k + 32 <= s1) && c0 + c >= sh;
                         uint32_t vis = 0xffffffffu;
@@ -395,8 +402,10 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                                 v = (vis >> (e + 1)) & 1u ? v : 0.f;
                             }
                             pk[e / 2] = pack_bf16(u, v);
+                            if constexpr (SPLIT) pr[e / 2] = pack2_rest<T>(u, v, pk[e / 2]);
                         }
                         atc::tmem_st16(tS + c / 2, pk);
+                        if constexpr (SPLIT) atc::tmem_st16(tS + 32 + c / 2, pr);
                     }
                 }
                 if (!sum) {
@@ -576,7 +585,7 @@ struct SkSmem {
     static constexpr int ALLOC = TOTAL + 1024;
 };
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(SB_THREADS, 1)
     sink_dkv_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap domap,
                        const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -760,13 +769,16 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                     const uint64_t b = qd + st * 2 * USTEP;
                     const uint32_t acc = info & TI_FIRST ? 0u : 1u;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tc::mma_bf16_ts(tmem + KVT_V, tmem + KVT_S + g * 128 + c * 8, b + USTEP + c * 128, ID_O,
-                                        c > 0 ? 1u : acc);
+                    for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tc::mma_bf16_ts(tmem + KVT_K, tmem + KVT_S + g * 128 + 64 + c * 8, b + c * 128, ID_O,
-                                        c > 0 ? 1u : acc);
+                        for (int c = 0; c < 4; ++c)
+                            tc::mma_bf16_ts(tmem + KVT_V, tmem + KVT_S + g * 128 + part * 32 + c * 8, b + USTEP + c * 128, ID_O,
+                                            c + part > 0 ? 1u : acc);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            tc::mma_bf16_ts(tmem + KVT_K, tmem + KVT_S + g * 128 + 64 + part * 32 + c * 8, b + c * 128, ID_O,
+                                            c + part > 0 ? 1u : acc);
+                    }
                     tc::mma_commit(pd_done + g);
                     tc::mma_commit(q_empty + st);
                     if (info & TI_LAST) tc::mma_commit(acc_full);
@@ -845,12 +857,25 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                     tc::fence_proxy_async_smem();
                 }
                 const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+                uint32_t s1[SPLIT ? 32 : 1], dp1[SPLIT ? 32 : 1];
+                if constexpr (SPLIT) {                    // the rests of the first columns go over these
+                    tmem_ld32(tS + 32, s1);
+                    tmem_ld32(tP + 32, dp1);
+                }
 #pragma unroll
                 for (int c = 0; c < 64; c += 32) {
-                    uint32_t s[32], dp[32], pk[16], dk[16];
-                    tmem_ld32(tS + c, s);
-                    tmem_ld32(tP + c, dp);
-                    tc::tmem_ld_wait();
+                    uint32_t s[32], dp[32], pk[16], dk[16], pr[16], dr[16];
+                    if (SPLIT && c > 0) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            s[e] = s1[SPLIT ? e : 0];
+                            dp[e] = dp1[SPLIT ? e : 0];
+                        }
+                    } else {
+                        tmem_ld32(tS + c, s);
+                        tmem_ld32(tP + c, dp);
+                        tc::tmem_ld_wait();
+                    }
                     const uint32_t vis = clear ? 0xffffffffu : bit_range(va - c, vb - c);
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
@@ -870,9 +895,17 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                         }
                         pk[e / 2] = pack_bf16(a, b);
                         dk[e / 2] = pack_bf16(x0, x1);
+                        if constexpr (SPLIT) {
+                            pr[e / 2] = pack2_rest<T>(a, b, pk[e / 2]);
+                            dr[e / 2] = pack2_rest<T>(x0, x1, dk[e / 2]);
+                        }
                     }
                     atc::tmem_st16(tS + c / 2, pk);
                     atc::tmem_st16(tP + c / 2, dk);
+                    if constexpr (SPLIT) {
+                        atc::tmem_st16(tS + 32 + c / 2, pr);
+                        atc::tmem_st16(tP + 32 + c / 2, dr);
+                    }
                 }
                 atc::tmem_st_wait();
                 tc::fence_before_sync();

@@ -11,7 +11,9 @@
 // with the running maximum m and sum of a row held by one thread; P replaces
 // S in tensor memory and is the A operand of the second product.  m is raised
 // (and O rescaled) only when a tile exceeds it by more than 2^8.  P is
-// rounded to the inputs' type (half a step a weight, as the output is).
+// rounded to the inputs' type (half a step a weight, as the output is); with
+// SPLIT what that leaves enters as a second product, so that the output's own
+// rounding is all that remains.
 //
 // The tensor cores and the softmax alternate between A and B: while one
 // tile's scores are turned into weights the other's products run.  S and P of
@@ -26,7 +28,8 @@
 //
 // Rows of V that not every row of the item sees are cleaned in shared memory
 // first: 0 * inf would put NaN into rows that must not see them.  What is not
-// finite there is added back, at the end, to the rows that do see it.
+// finite there is added back, at the end, to the rows that do see it.  (With
+// SPLIT every row is: the two parts of a weight times inf are inf - inf.)
 //
 // Warps: 0-3 softmax and epilogue of A (thread = row), 4-7 of B, 8 TMA
 // producer, 9 and 10 MMA issuers of A and B (9 also owns the TMEM).  Every wait is bounded; a timeout
@@ -236,6 +239,12 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+// What rounding two values to T leaves, as a packed pair.
+template <typename T>
+__device__ __forceinline__ unsigned pack2_rest(float lo, float hi, unsigned packed) {
+    const T *q = reinterpret_cast<const T *>(&packed);
+    return pack2<T>(lo - to_f(q[0]), hi - to_f(q[1]));
+}
 // one lane of a converged warp
 __device__ __forceinline__ bool elect_one() {
     uint32_t ok;
@@ -278,7 +287,7 @@ struct alignas(16) SfItem {
 // beside it: columns / 16, who uses it, where its item begins and ends.
 enum : uint32_t { TI_STEPS = 15u, TI_A = 16u, TI_B = 32u, TI_FIRST = 64u, TI_LAST = 128u, TI_TILE = 256u };
 
-template <typename T, int D>
+template <typename T, int D, bool SPLIT>
 __global__ void __launch_bounds__(SF_THREADS, 1)
     sink_fwd_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ KeyMaps kmap,
                        const __grid_constant__ KeyMaps vmap, const __grid_constant__ SinkParams p,
@@ -403,6 +412,12 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                         for (int c = 0; c < 4; ++c)
                             if (c < steps)
                                 tc::mma_bf16_ts(tO, tS + h * 64 + c * 8, v + (4 * h + c) * 128, ID_O, c > 0 ? 1u : begun);
+                        if constexpr (SPLIT) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                if (c < steps)
+                                    tc::mma_bf16_ts(tO, tS + h * 64 + 32 + c * 8, v + (4 * h + c) * 128, ID_O, 1u);
+                        }
                         tc::mma_commit(pv_done + 2 * I + h);
                     }
                     ppar ^= 1u << h;
@@ -559,9 +574,9 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                 const int sh = in_sink ? head : 0;         // rows of the tile that the sinks share
                 // clean the rows of V that not every row of the item sees.  Both row tiles do, each before its own
                 // P: their products are issued by different warps, and cleaning twice changes nothing
-                if (k0 + sh < cl || k0 + n16 > ch || sh > x.s_end) {
+                if (SPLIT || k0 + sh < cl || k0 + n16 > ch || sh > x.s_end) {
                     const uint32_t kt = kt0 + j;
-                    const int sl = 2 * (kt & 1) + 1, ca = min(n, max(0, cl - k0)), cb = min(n, max(0, ch - k0));
+                    const int sl = 2 * (kt & 1) + 1, ca = SPLIT ? n : min(n, max(0, cl - k0)), cb = min(n, max(0, ch - k0));
                     if (!wait_warp(kv_full + sl, (kt >> 1) & 1, abort_flag)) { ok = false; break; }
                     // 16-byte units of the rows [0, ca) and [cb, n16)
                     constexpr int U = D / 8;
@@ -571,10 +586,10 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                         int key = u / U;
                         const int c = u % U;
                         if (key >= ca) key += gap;
-                        if (key < sh && key < x.s_end) continue;
+                        if (!SPLIT && key < sh && key < x.s_end) continue;
                         uint4 *at = reinterpret_cast<uint4 *>(smem + L::OFF_KV + sl * L::TILE + (c / 8) * (SF_KT * 128) +
                                                               key * 128 + (((c & 7) ^ (key & 7)) * 16));
-                        if (key >= n || key < sh) {
+                        if (key >= n || (key < sh && key >= x.s_end)) {
                             *at = make_uint4(0u, 0u, 0u, 0u);
                             continue;
                         }
@@ -658,7 +673,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                     uint64_t rs[2] = {0ull, 0ull};
 #pragma unroll
                     for (int c = 0; c < 64; c += 32) {
-                        uint32_t pk[16];
+                        uint32_t pk[16], pr[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             float p0, p1;
@@ -668,8 +683,10 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                             p1 = ex2_fast(p1);
                             rs[(e >> 1) & 1] = f2_add(rs[(e >> 1) & 1], f2_pack(p0, p1));
                             pk[e / 2] = pack2<T>(p0, p1);
+                            if constexpr (SPLIT) pr[e / 2] = pack2_rest<T>(p0, p1, pk[e / 2]);
                         }
                         atc::tmem_st16(tS + c0 + c / 2, pk);
+                        if constexpr (SPLIT) atc::tmem_st16(tS + c0 + 32 + c / 2, pr);
                     }
                     float r0, r1;
                     f2_unpack(f2_add(rs[0], rs[1]), r0, r1);
@@ -724,8 +741,12 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
                         const T *vb = (const T *)p.v + (p.cu_q ? 0 : b) * p.v_s[0] + sq.k0 * p.v_s[1] +
                                       (x.heads & 0xfffff) / p.G * p.v_s[2] + c0;
 #pragma unroll 1
-                        for (int k = x.band_lo; k < x.band_hi; ++k) {
-                            if (k == x.clean_lo && k < x.clean_hi) k = x.clean_hi;
+                        for (int k = SPLIT ? 0 : x.band_lo; k < x.band_hi; ++k) {
+                            if (SPLIT) {
+                                if (k >= x.s_end && k < x.band_lo) k = x.band_lo;
+                            } else if (k == x.clean_lo && k < x.clean_hi) {
+                                k = x.clean_hi;
+                            }
                             if (k >= x.band_hi) break;
                             if (!(k < s1 || (k >= lo && k < hi))) continue;
 #pragma unroll
