@@ -207,7 +207,7 @@ static SinkKvTiles sink_kv_tiles(const SinkParams &p) {
         t.n_split = (int)std::min(most, (nq + want - 1) / want);
         t.tps = (int)((nq + t.n_split - 1) / t.n_split);
     }
-    t.items = (int)((t.band + (long long)p.B * t.n_kt * t.n_split) * p.Hkv);
+    t.items = (int)std::min<long long>((t.band + (long long)p.B * t.n_kt * t.n_split) * p.Hkv, INT_MAX);
     return t;
 }
 struct SinkBwdLayout { size_t counter, part, total; };
@@ -301,6 +301,8 @@ extern "C" int sa_sink_attn_bwd(const sa_sink_shape *shape, const void *q, const
     SinkParams p = sink_params(shape, q, k, v, cu_q, cu_k);
     rc = device_error_word(&p.err);
     if (rc) return rc;
+    if (sink_kv_tiles(p).items >= INT_MAX / 2)
+        return fail(SA_ERR_UNSUPPORTED, "sink_attn_bwd: too many sequences for so many sinks (give max_k)");
     p.lse_in = lse; p.dout = dout;
     p.dq = dq; p.dk = dk; p.dv = dv; p.stat = static_cast<float2 *>(workspace);
     if (shape->Tq == 0 && shape->L == 0) return SA_OK;

@@ -50,13 +50,14 @@ struct SqSmem {
     static constexpr int OFF_V = OFF_K + 2 * TILE;         // 1
     static constexpr int OFF_BAR = OFF_V + TILE;
     // q_full[2], q_empty[2], k_full[2], k_empty[2], v_full, v_empty, dp_full, dp_free, ds_full[2],
-    // dq_full, drain[2], item_full[2], item_empty[2]
-    static constexpr int N_BAR = 22;
+    // dq_full, drain[2], item_full[2], item_empty[2], d_full
+    static constexpr int N_BAR = 24;                       // 22, to keep the items on 16 bytes
     static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;   // tmem slot, abort flag, -, -, tile info[2]
     static constexpr int OFF_ITEM = OFF_MISC + 32;
     static constexpr int OFF_D = OFF_ITEM + 2 * 64;        // [2][128] halves of D
     static constexpr int TOTAL = OFF_D + 1024;
     static constexpr int ALLOC = TOTAL + 1024;
+    static_assert(OFF_ITEM % 16 == 0 && ALLOC <= 232448, "items are copied by 16 bytes; 227 KB per CTA");
     static_assert(8 * 32 * D <= 2 * TILE, "the staged rows fit the item's Q and dO");
 };
 
@@ -75,6 +76,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     uint64_t *q_full = bars, *q_empty = bars + 2, *k_full = bars + 4, *k_empty = bars + 6, *v_full = bars + 8;
     uint64_t *v_empty = bars + 9, *dp_full = bars + 10, *dp_free = bars + 11, *ds_full = bars + 12;
     uint64_t *dq_full = bars + 14, *drain = bars + 15, *item_full = bars + 17, *item_empty = bars + 19;
+    uint64_t *d_full = bars + 21;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
     volatile uint32_t *info_s = reinterpret_cast<volatile uint32_t *>(smem + L::OFF_MISC + 16);
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         }
         tc::mbar_init(v_full, 1); tc::mbar_init(v_empty, 1);
         tc::mbar_init(dp_full, 1); tc::mbar_init(dp_free, 8);
-        tc::mbar_init(dq_full, 1);
+        tc::mbar_init(dq_full, 1); tc::mbar_init(d_full, 8);
         *abort_flag = 0;
         tc::mbar_fence_init();
     }
@@ -322,7 +324,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                     float *xd = reinterpret_cast<float *>(smem + L::OFF_D), d0, d1;
                     f2_unpack(f2_add(dsum[0], dsum[1]), d0, d1);
                     xd[w * 128 + r] = d0 + d1;
-                    atc::named_sync(1, 256);
+                    // (an mbarrier: a warp that gave up must not leave the others waiting without a limit)
+                    arrive_warp(d_full);
+                    if (!wait_warp(d_full, qn & 1, abort_flag)) { ok = false; break; }
                     Dr = xd[r] + xd[128 + r];
                     if (w == 0 && row_ok) p.stat[row0 + row_at] = make_float2(-nl, Dr);
                 }
@@ -577,12 +581,13 @@ struct SkSmem {
     static constexpr int OFF_STAT = OFF_STAGE + 8 * 4096;  // [group][2][64] lse, D
     static constexpr int OFF_BAR = OFF_STAT + 4 * 64 * 8;
     // kv_full, kv_empty, q_full[S], q_empty[S], sd_full[2], pd_full[2], pd_done[2], acc_full, acc_free, drain[2],
-    // item_full[2], item_empty[2]
-    static constexpr int N_BAR = 14 + 2 * KVT_STAGES;
+    // item_full[2], item_empty[2], stat_full[2]
+    static constexpr int N_BAR = 16 + 2 * KVT_STAGES;
     static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;   // tmem slot, abort flag, -, -, unit info[S]
     static constexpr int OFF_ITEM = OFF_MISC + 32;
     static constexpr int TOTAL = OFF_ITEM + 2 * 64;
     static constexpr int ALLOC = TOTAL + 1024;
+    static_assert(OFF_ITEM % 16 == 0 && ALLOC <= 232448, "items are copied by 16 bytes; 227 KB per CTA");
 };
 
 template <int D, bool SPLIT>
@@ -600,6 +605,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     uint64_t *kv_full = bars, *kv_empty = bars + 1, *q_full = bars + 2, *q_empty = q_full + KVT_STAGES;
     uint64_t *sd_full = q_empty + KVT_STAGES, *pd_full = sd_full + 2, *pd_done = pd_full + 2, *acc_full = pd_done + 2;
     uint64_t *acc_free = acc_full + 1, *drain = acc_free + 1, *item_full = drain + 2, *item_empty = item_full + 2;
+    uint64_t *stat_full = item_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
     volatile uint32_t *info_s = reinterpret_cast<volatile uint32_t *>(smem + L::OFF_MISC + 16);
@@ -614,6 +620,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         for (int i = 0; i < KVT_STAGES; ++i) { tc::mbar_init(q_full + i, 1); tc::mbar_init(q_empty + i, 1); }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(sd_full + i, 1); tc::mbar_init(pd_full + i, 4); tc::mbar_init(pd_done + i, 1);
+            tc::mbar_init(stat_full + i, 4);
             tc::mbar_init(drain + i, 1);
             tc::mbar_init(item_full + i, 1); tc::mbar_init(item_empty + i, 8);
         }
@@ -831,7 +838,8 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                 const int u = u0 + i;
                 float2 *sm = stat_s + ((u >> 1) & 1) * 64;
                 if (col < 64) sm[col] = make_float2(-mine.x, -mine.y);
-                atc::named_sync(1 + g, 128);
+                arrive_warp(stat_full + g);           // bounded, as every wait between warps here
+                if (!wait_warp(stat_full + g, (u >> 1) & 1, abort_flag)) { ok = false; break; }
                 mine = fetch(i + 2);
                 const int t0 = x.ta + (tl.HC == 1 ? i : i / tl.HC) * tl.TPT;
                 if (!wait_warp(sd_full + g, (u >> 1) & 1, abort_flag)) { ok = false; break; }

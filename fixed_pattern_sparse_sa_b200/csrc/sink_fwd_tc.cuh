@@ -66,6 +66,7 @@ struct SfSmem {
     static constexpr int OFF_ITEM = OFF_MISC + 32;         // two work items of the softmax warps
     static constexpr int TOTAL = OFF_ITEM + 2 * 64;
     static constexpr int ALLOC = TOTAL + 1024;
+    static_assert(OFF_ITEM % 16 == 0 && ALLOC <= 232448, "items are copied by 16 bytes; 227 KB per CTA");
 };
 
 struct SinkTiles {
