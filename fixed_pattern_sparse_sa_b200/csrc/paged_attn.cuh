@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const PagedPar
         } while (x.s.nch == 0);
     };
     unsigned vmask[PD_STAGES];                // visible, well-paged keys of the chunk in each stage
-    // chunk x into ring stage st: lane i < 16 finds key i's page and slot
+    // chunk x into ring stage st: lanes i and i + 16 find key i's page and slot, one for K, one for V
+    const long long page_s = lane < 16 ? p.k_s[0] : p.v_s[0], slot_s = lane < 16 ? p.k_s[1] : p.v_s[1];
     auto load = [&](const Pos &x, int st) -> unsigned {
         const int i = x.c * PD_NK + (lane & 15);
         bool ok = i < x.s.n_vis;
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const PagedPar
             }
         }
         const unsigned mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+        const long long row = pg * page_s + slot * slot_s;
         const int hk = x.h2 / p.HT;
         const T *kb = (const T *)p.k + hk * p.k_s[2], *vb = (const T *)p.v + hk * p.v_s[2];
         const uint32_t dst = ring_a + st * L::STAGE;
@@ -218,11 +220,11 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const PagedPar
 #pragma unroll
         for (int r0 = 0; r0 < PD_NK; r0 += RPI) {
             const int r = r0 + lane / U;
-            const long long pr = __shfl_sync(0xffffffffu, pg, r), sr = __shfl_sync(0xffffffffu, slot, r);
+            const long long kr = __shfl_sync(0xffffffffu, row, r), vr = __shfl_sync(0xffffffffu, row, r + 16);
             const int bytes = (mask >> r) & 1 ? 16 : 0;
             const uint32_t at = dst + r * (D * 2) + ((u ^ (r & 7)) * 16);
-            cp_async16_at<0, 0>(at, kb + pr * p.k_s[0] + sr * p.k_s[1] + u * 8, bytes);
-            cp_async16_at<L::TILE, 0>(at, vb + pr * p.v_s[0] + sr * p.v_s[1] + u * 8, bytes);
+            cp_async16_at<0, 0>(at, kb + kr + u * 8, bytes);
+            cp_async16_at<L::TILE, 0>(at, vb + vr + u * 8, bytes);
         }
         return mask;
     };
