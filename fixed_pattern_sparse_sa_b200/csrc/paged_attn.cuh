@@ -21,6 +21,10 @@
 // P enters the second product as two values of the caches' type, its rounding
 // and what that leaves (16 to 22 bits), so that a row of few keys is as exact
 // as its output's type; the bytes bind, not the products.  All sums are fp32.
+//
+// Measured on one B200: 32 sequences of 128K, 16 heads on one KV head, 378 us =
+// 5.7 TB/s (87 % of a copy's rate); 192 ragged sequences, window 4096 and 64
+// sinks, 64 heads on 8, 349 us = 5.2 TB/s.
 #pragma once
 
 #include "sa_common.cuh"
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const PagedPar
 #pragma unroll
         for (int e = 0; e < CPT; ++e) acc[e] += f * src[e];
     }
-    // whose item: warp 0 is busy whenever any warp of a single-item CTA is... its start is the CTA's
+    // the CTA's one item
     const int b = start_b[PD_NW - 1];         // the last warp's share is never empty
     const PdSeq s = pd_seq(p, b, false);
     const long long i0 = (ca - scan[2 * PD_NW - 1] * H2) / s.nch;

@@ -432,7 +432,8 @@ int sa_sink_attn_bwd(const sa_sink_shape *shape, const void *q, const void *k, c
  * as in sa_sink_attn_fwd: window = 0 sees every key (sinks then says nothing),
  * else p - j < window or j < sinks.  Table entries of pages without a visible
  * key are not read (they may be -1: a trimmed middle), nor are slots without
- * one, whatever they hold.  n = 0 gives out = 0, lse = -inf.
+ * one, whatever they hold.  n = 0 gives out = 0, lse = -inf.  (An infinity in
+ * a visible v makes its column NaN.)
  *   q [B, Hq, d]; caches [n_pages, page, Hkv, d] (bf16 or fp16); block_table
  *   int32 [B, max_pages], seq_lens int32 [B] (device).  q, k_cache and v_cache
  *   are strided (q: batch, head; caches: page, slot, head; multiples of 8
@@ -559,9 +560,10 @@ int sa_check_device_status(void *stream);
  *   the default (2e9, about one second).  Waits that drain a kernel's own
  *   copies and MMAs before it frees tensor memory keep a fixed long limit.
  * sa_debug_inject_stall: while on != 0, the NSA tensor-core branch kernels
- *   (head dim 128) issue none of their loads, so each CTA's first wait is on
- *   a barrier that nothing completes; it runs out after the spin limit and
- *   sa_nsa_fwd's outputs are undefined.  Nothing is left in flight.
+ *   (head dim 128) and the sink-window kernels issue none of their loads, so
+ *   each CTA's first wait is on a barrier that nothing completes; it runs out
+ *   after the spin limit and the outputs of sa_nsa_fwd, sa_sink_attn_fwd and
+ *   sa_sink_attn_bwd are undefined.  Nothing is left in flight.
  * sa_debug_exact_recompute_rows: synchronizes the current device and returns
  *   the number of rows whose top-k sa_indexer_topk took by exact recompute
  *   (the sampled-threshold candidate list was short or overflowed) since the

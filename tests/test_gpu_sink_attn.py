@@ -292,3 +292,27 @@ def test_refusals(cuda_ok):
     with pytest.raises(ValueError):
         api.sink_attn_bwd(q, k, v, out, lse[:, :16], q, 4)
     api.check_device_status()
+
+
+def test_a_wait_that_runs_out_is_reported(cuda_ok):
+    # the stall hook keeps the kernels from loading anything: their first waits run out after the spin limit
+    q, k, v = _dense(1, 600, 600, 8, 2, 128, BF, 16)
+    dout = torch.randn(q.shape, device="cuda").to(BF)
+    want = api.sink_attn_fwd(q, k, v, 100, 4)
+    wantg = api.sink_attn_bwd(q, k, v, *want, dout, 100, 4)
+    api.check_device_status()
+    for call in (lambda: api.sink_attn_fwd(q, k, v, 100, 4), lambda: api.sink_attn_bwd(q, k, v, *want, dout, 100, 4)):
+        try:
+            api.debug_set_spin_limit(20_000_000)                  # about 10 ms
+            api.debug_inject_stall(True)
+            call()
+            with pytest.raises(api.SAError) as e:
+                api.check_device_status()
+            assert e.value.status == _lib.SA_ERR_TIMEOUT
+        finally:
+            api.debug_inject_stall(False)
+            api.debug_set_spin_limit(0)
+        got = api.sink_attn_fwd(q, k, v, 100, 4)
+        gotg = api.sink_attn_bwd(q, k, v, *got, dout, 100, 4)
+        api.check_device_status()
+        assert all(torch.equal(a, b) for a, b in zip((*want, *wantg), (*got, *gotg)))
