@@ -95,9 +95,10 @@ __device__ __forceinline__ int pb_entry(const int32_t *ends, int n, int r) {
     }
     return lo;
 }
-// Running sums of need(i) over the list, written to ends (and to smem while
-// they fit); by CTA 0 of the cluster.  Capped at n_pages + 1: no comparison
-// with a number of free pages tells larger values apart.
+// Running sums of need(i) over the list, written to ends; by CTA 0 of the
+// cluster.  Capped at n_pages + 1: no comparison with a number of free pages
+// tells larger values apart.  Two neighbours at the cap do look alike, so
+// whether an entry needs pages is never read off a difference of ends.
 template <typename F>
 __device__ __forceinline__ void pb_ends(const BooksParams &p, int *warp_sums, F &&need) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -124,6 +125,11 @@ __device__ __forceinline__ void pb_ends(const BooksParams &p, int *warp_sums, F 
     }
 }
 
+// Pages that `add` tokens behind the first `old` take beyond those of the first.
+__device__ __forceinline__ int pb_more(int page, int old, int add) {
+    return (int)(((long long)old + add + page - 1) / page - ((long long)old + page - 1) / page);
+}
+
 __global__ void __cluster_dims__(PB_CTAS, 1, 1) __launch_bounds__(PB_THREADS) paged_extend_kernel(const BooksParams p) {
     grid_dependency_sync();
     __shared__ int counts[32], warp_sums[32];
@@ -147,8 +153,7 @@ __global__ void __cluster_dims__(PB_CTAS, 1, 1) __launch_bounds__(PB_THREADS) pa
             const bool fits = ok && (long long)old + add <= cap;
             if (!ok) raise_error(p.err, ERR_BAD_INDEX);
             p.seq[i] = fits ? s : -1;
-            if (!fits) return 0;
-            return (int)(((long long)old + add + p.page - 1) / p.page - ((long long)old + p.page - 1) / p.page);
+            return fits ? pb_more(p.page, old, add) : 0;
         });
     }
     int n_free;
@@ -171,11 +176,14 @@ __global__ void __cluster_dims__(PB_CTAS, 1, 1) __launch_bounds__(PB_THREADS) pa
     cl.sync();                                                 // every length has been read
     if (cl.block_rank() == 0)
         for (int i = tid; i < p.n; i += PB_THREADS) {
-            const int s = p.seq[i], e = ends[i], first = i > 0 ? ends[i - 1] : 0;
+            const int s = p.seq[i];
             int st = -1;
-            if (s >= 0 && (e <= n_free || e == first)) {
-                st = p.lens[s];
-                p.lens[s] = st + p.c[i];
+            if (s >= 0) {
+                const int old = p.lens[s], add = p.c[i];
+                if (ends[i] <= n_free || pb_more(p.page, old, add) == 0) {
+                    st = old;
+                    p.lens[s] = old + add;
+                }
             }
             p.result[i] = st;
         }
@@ -238,10 +246,10 @@ __global__ void __cluster_dims__(PB_CTAS, 1, 1) __launch_bounds__(PB_THREADS) pa
     // the shared pages: one warp per entry; the fresh page's place is the walk's
     for (int i = (int)cl.block_rank() * 32 + (tid >> 5); i < p.n; i += PB_WARPS) {
         const int s = p.seq[i];
-        const int first = i > 0 ? ends[i - 1] : 0;
-        const bool tail = ends[i] > first;
-        if (s < 0 || (tail && ends[i] > n_free)) continue;
-        const int d = p.c[i], full = p.lens[s] / p.page;
+        if (s < 0) continue;
+        const int d = p.c[i], len = p.lens[s], full = len / p.page;
+        const bool tail = len % p.page != 0;
+        if (tail && ends[i] > n_free) continue;
         for (int k = lane; k < p.max_pages; k += 32) {
             if (tail && k == full) continue;
             int id = -1;
@@ -256,9 +264,9 @@ __global__ void __cluster_dims__(PB_CTAS, 1, 1) __launch_bounds__(PB_THREADS) pa
     // dst lengths: no dst is a src, so nothing above reads them
     if (cl.block_rank() == 0)
         for (int i = tid; i < p.n; i += PB_THREADS) {
-            const int s = p.seq[i], first = i > 0 ? ends[i - 1] : 0;
-            const bool ok = s >= 0 && (ends[i] == first || ends[i] <= n_free);
-            if (ok) p.lens[p.c[i]] = p.lens[s];
+            const int s = p.seq[i], len = s >= 0 ? p.lens[s] : 0;
+            const bool ok = s >= 0 && (len % p.page == 0 || ends[i] <= n_free);
+            if (ok) p.lens[p.c[i]] = len;
             p.result[i] = ok;
         }
 }
