@@ -196,6 +196,26 @@ __global__ void __cluster_dims__(PB_CTAS, 1, 1) __launch_bounds__(PB_THREADS) pa
     cg::cluster_group cl = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31;
     auto in = [&](int s) { return s >= 0 && s < p.S; };
+    auto held = [&](int s, int &len) -> bool {                // a sequence whose length its row can hold
+        len = in(s) ? p.lens[s] : -1;
+        return len >= 0 && (long long)len <= (long long)p.max_pages * p.page;
+    };
+    // an entry whose row names a page outside the pool is refused before any page is counted for it: a warp per
+    // entry looks its row over (to[i] = 1 where it does)
+    for (int i = (int)cl.block_rank() * 32 + (tid >> 5); i < p.n; i += PB_WARPS) {
+        const int s = p.a[i];
+        int len;
+        bool out = false;
+        if (held(s, len)) {
+            const int32_t *row = p.table + (size_t)s * p.max_pages;
+            const int pages = (int)(((long long)len + p.page - 1) / p.page);
+#pragma unroll 8
+            for (int k = lane; k < pages; k += 32) out |= row[k] >= p.n_pages;
+        }
+        out = __any_sync(0xffffffffu, out);
+        if (lane == 0) p.to[i] = out;
+    }
+    cl.sync();
     if (cl.block_rank() == 0) {
         for (int i = tid; i < p.n; i += PB_THREADS) {
             if (in(p.c[i])) { p.owner[p.c[i]] = INT_MAX; p.srcmark[p.c[i]] = 0; }
@@ -209,17 +229,10 @@ __global__ void __cluster_dims__(PB_CTAS, 1, 1) __launch_bounds__(PB_THREADS) pa
         __syncthreads();
         pb_ends(p, warp_sums, [&](int i) -> int {
             const int s = p.a[i], d = p.c[i];
-            bool ok = in(s) && in(d) && p.owner[d] == i && p.owner[s] == INT_MAX && p.srcmark[d] == 0 && p.lens[d] == 0;
-            int len = 0, need = 0;
-            if (ok) {
-                len = p.lens[s];
-                ok = len >= 0 && (long long)len <= (long long)p.max_pages * p.page;
-            }
-            if (ok && len % p.page) {
-                const int old = p.table[(size_t)s * p.max_pages + len / p.page];
-                ok = old >= 0 && old < p.n_pages;
-                need = ok;
-            }
+            int len, need = 0;
+            bool ok = held(s, len) && in(d) && p.owner[d] == i && p.owner[s] == INT_MAX && p.srcmark[d] == 0 &&
+                      p.lens[d] == 0 && p.to[i] == 0;
+            if (ok && len % p.page) need = ok = p.table[(size_t)s * p.max_pages + len / p.page] >= 0;
             if (!ok) raise_error(p.err, ERR_BAD_INDEX);
             p.seq[i] = ok ? s : -1;
             p.from[i] = p.to[i] = -1;
@@ -255,7 +268,6 @@ __global__ void __cluster_dims__(PB_CTAS, 1, 1) __launch_bounds__(PB_THREADS) pa
             int id = -1;
             if (k < full) {
                 id = p.table[(size_t)s * p.max_pages + k];
-                if (id >= p.n_pages) { raise_error(p.err, ERR_BAD_INDEX); id = -1; }
                 if (id >= 0 && atomicAdd(&p.refcount[id], 1) <= 0) raise_error(p.err, ERR_BAD_INDEX);
             }
             p.table[(size_t)d * p.max_pages + k] = id;

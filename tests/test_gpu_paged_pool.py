@@ -4,7 +4,7 @@ of the books."""
 import pytest
 import torch
 
-from fixed_pattern_sparse_sa_b200 import api
+from fixed_pattern_sparse_sa_b200 import _lib, api
 from test_gpu_paged import BF, _books, _i32
 
 pytestmark = pytest.mark.gpu
@@ -63,5 +63,28 @@ def test_fork_asks_for_more_than_the_pool(cuda_ok, tails, whole, spare):
     _same(model, table, lt, rc)
     if moves:
         s, d = (torch.tensor(x, device="cuda") for x in zip(*moves))
+        want[d] = want[s]
+    assert torch.equal(cache, want)
+
+
+@pytest.mark.parametrize("at", [0, 1, 70, 71])                       # the last one: the partly filled page
+@pytest.mark.parametrize("bad", [0, 5, 2 ** 31 - 1])
+def test_fork_of_a_row_that_names_a_page_outside_the_pool(cuda_ok, at, bad):
+    # the entry is refused as a whole: its row, length, counts and pages stay, and its page goes to no other
+    page, lens = 4, [70 * 4 + 7, 9, 6, 0, 0, 0, 0]
+    table, lt, rc, model = _books(lens, page, 80, 3, 33)
+    bad = min(rc.shape[0] + bad, 2 ** 31 - 1)
+    table[0, at] = model.t[0][at] = bad
+    cache = torch.randn((rc.shape[0], page, 8), device="cuda").to(BF)
+    want = cache.clone()
+    src, dst = [1, 0, 2, 0], [3, 4, 5, 6]
+    done = api.paged_fork(table, lt, rc, _i32(src), _i32(dst), page, [cache])
+    with pytest.raises(api.SAError) as e:
+        api.check_device_status()
+    assert e.value.status == _lib.SA_ERR_DEVICE_ASSERT
+    ok, moves = model.fork([1, 2], [3, 5])
+    assert ok == [1, 1] and done.tolist() == [1, 0, 1, 0]
+    _same(model, table, lt, rc)
+    for s, d in moves:
         want[d] = want[s]
     assert torch.equal(cache, want)
