@@ -18,9 +18,11 @@
 // one item merges its warps in shared memory; what remains spans several
 // warps or CTAs and is joined by paged_join_kernel from fp32 partials.
 //
-// P enters the second product as two values of the caches' type, its rounding
-// and what that leaves (16 to 22 bits), so that a row of few keys is as exact
-// as its output's type; the bytes bind, not the products.  All sums are fp32.
+// P enters the second product as two values of the caches' type, rounded
+// towards zero and what that leaves (16 to 22 bits), so that a row of few keys
+// is as exact as its output's type; the bytes bind, not the products.  Both
+// parts are above 0, so an infinity in a visible V stays one (0 * inf, or
+// parts of different signs, would make it NaN).  All sums are fp32.
 //
 // Measured on one B200: 32 sequences of 128K, 16 heads on one KV head, 378 us =
 // 5.7 TB/s (87 % of a copy's rate); 192 ragged sequences, window 4096 and 64
@@ -38,6 +40,9 @@ constexpr int PD_STAGES = 2;              // ring stages per warp: one chunk in 
 constexpr int PD_THREADS = PD_NW * 32;
 constexpr int PD_MIN_CHUNKS = 2;          // chunks per warp below which fewer CTAs share the list
 constexpr float PD_RAISE = 8.f;           // log2 headroom before the accumulators are rescaled
+// log2 of the largest weight when it is taken.  fp16 holds nothing below 2^-24:
+// at 2^7 to 2^15 of its 2^16 a weight of 2^-17 of the largest still has 14 bits.
+template <typename T> constexpr float PD_TOP = std::is_same<T, __half>::value ? 7.f : 0.f;
 
 template <int D>
 struct PdSmem {
@@ -102,6 +107,23 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const unsigned (&a)[4],
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
 }
+// Two weights >= 0 as packed pairs a + b: a rounded towards zero, b what that
+// leaves, but no less than the type's least (normal bf16, fp16) value.
+template <typename T>
+__device__ __forceinline__ void split_up(float x, float y, unsigned &a, unsigned &b) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const unsigned xi = __float_as_uint(x), yi = __float_as_uint(y);
+        a = __byte_perm(xi, yi, 0x7632);
+        b = pack2<T>(fmaxf(x - __uint_as_float(xi & 0xffff0000u), 0x1p-126f),
+                     fmaxf(y - __uint_as_float(yi & 0xffff0000u), 0x1p-126f));
+    } else {
+        const __half xh = __float2half_rz(x), yh = __float2half_rz(y);
+        const __half2 h = __halves2half2(xh, yh);
+        a = *reinterpret_cast<const unsigned *>(&h);
+        b = pack2<T>(fmaxf(x - to_f(xh), 0x1p-24f), fmaxf(y - to_f(yh), 0x1p-24f));
+    }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const PagedParams p) {
     grid_dependency_sync();
@@ -358,6 +380,7 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const PagedPar
             for (int e = 0; e < 2; ++e) {
                 mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
                 mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+                mx[e] -= PD_TOP<T>;
                 alpha[e] = 1.f;
                 if (mx[e] > m[e] + (m[e] == -INFINITY ? 0.f : PD_RAISE)) {
                     alpha[e] = m[e] == -INFINITY ? 0.f : ex2_fast(m[e] - mx[e]);
@@ -385,12 +408,8 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const PagedPar
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float x = s[t][2 * e], y = s[t][2 * e + 1];
-                    const T xh = from_f<T>(x), yh = from_f<T>(y);
-                    pa[2 * t + e] = pack2<T>(x, y);
-                    pb[2 * t + e] = pack2<T>(x - to_f(xh), y - to_f(yh));
-                }
+                for (int e = 0; e < 2; ++e)
+                    split_up<T>(s[t][2 * e], s[t][2 * e + 1], pa[2 * t + e], pb[2 * t + e]);
             {
                 // V transposed: (keys 0-7, c 0-7), (keys 8-15, c 0-7), (keys 0-7, c 8-15), (keys 8-15, c 8-15)
                 const int r = (lane & 15), ub = lane >> 4;

@@ -432,8 +432,9 @@ int sa_sink_attn_bwd(const sa_sink_shape *shape, const void *q, const void *k, c
  * as in sa_sink_attn_fwd: window = 0 sees every key (sinks then says nothing),
  * else p - j < window or j < sinks.  Table entries of pages without a visible
  * key are not read (they may be -1: a trimmed middle), nor are slots without
- * one, whatever they hold.  n = 0 gives out = 0, lse = -inf.  (An infinity in
- * a visible v makes its column NaN.)
+ * one, whatever they hold.  n = 0 gives out = 0, lse = -inf.  An infinity in
+ * a visible v stays one in its column, as in sa_sink_attn_fwd (a weight that
+ * is 0 in fp32 makes it NaN).
  *   q [B, Hq, d]; caches [n_pages, page, Hkv, d] (bf16 or fp16); block_table
  *   int32 [B, max_pages], seq_lens int32 [B] (device).  q, k_cache and v_cache
  *   are strided (q: batch, head; caches: page, slot, head; multiples of 8
