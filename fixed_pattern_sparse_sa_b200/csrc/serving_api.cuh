@@ -440,8 +440,9 @@ static int books_params(const char *what, BooksParams &p, int32_t *table, int32_
     return device_error_word(&p.err);
 }
 
-// Checks the caches; vec: bytes of the widest vector that all of them allow.
-static int caches_check(const char *what, const sa_page_cache *caches, int n_caches, int64_t slot_bytes, int &vec) {
+// Checks the caches (of an empty pool a base may be null); vec: bytes of the widest vector that all of them allow.
+static int caches_check(const char *what, const sa_page_cache *caches, int n_caches, int64_t slot_bytes, int64_t n_pages,
+                        int &vec) {
     if (n_caches < 0 || slot_bytes < 0 || (n_caches > 0 && !caches))
         return fail(SA_ERR_INVALID_ARG, "%s: bad caches", what);
     vec = slot_bytes % 16 ? 4 : 16;
@@ -449,7 +450,7 @@ static int caches_check(const char *what, const sa_page_cache *caches, int n_cac
                                                     (long long)slot_bytes);
     for (int i = 0; i < n_caches; ++i) {
         const sa_page_cache &c = caches[i];
-        if (!c.base || c.page_stride < 0 || c.slot_stride < 0)
+        if ((!c.base && n_pages > 0) || c.page_stride < 0 || c.slot_stride < 0)
             return fail(SA_ERR_INVALID_ARG, "%s: cache %d", what, i);
         const unsigned long long bits = reinterpret_cast<uintptr_t>(c.base) | (unsigned long long)c.page_stride |
                                         (unsigned long long)c.slot_stride;
@@ -551,7 +552,7 @@ extern "C" int sa_paged_fork(int32_t *block_table, int32_t *seq_lens, int32_t *r
                              void *workspace, size_t workspace_bytes, void *stream) {
     SA_TRACE("sa_paged_fork");
     int rc = books_check("paged_fork", block_table, seq_lens, refcount, S, max_pages, n_pages, page, n), vec = 16;
-    if (rc == SA_OK) rc = caches_check("paged_fork", caches, n_caches, slot_bytes, vec);
+    if (rc == SA_OK) rc = caches_check("paged_fork", caches, n_caches, slot_bytes, n_pages, vec);
     if (rc) return rc;
     if (n == 0) return SA_OK;
     if (!src || !dst || !done || !aligned4(src) || !aligned4(dst) || !aligned4(done))
@@ -593,7 +594,7 @@ extern "C" int sa_paged_compact(int32_t *block_table, int32_t *refcount, int S, 
     int vec = 16;
     int rc = books_check("paged_compact", block_table, block_table ? (void *)block_table : (void *)n_live, refcount, S,
                          max_pages, n_pages, page, 0);
-    if (rc == SA_OK) rc = caches_check("paged_compact", caches, n_caches, slot_bytes, vec);
+    if (rc == SA_OK) rc = caches_check("paged_compact", caches, n_caches, slot_bytes, n_pages, vec);
     if (rc) return rc;
     if (!n_live || !aligned4(n_live)) return fail(SA_ERR_INVALID_ARG, "paged_compact: null or misaligned pointer");
     BooksParams p{};

@@ -88,3 +88,15 @@ def test_fork_of_a_row_that_names_a_page_outside_the_pool(cuda_ok, at, bad):
     for s, d in moves:
         want[d] = want[s]
     assert torch.equal(cache, want)
+
+
+def test_an_empty_pool_with_caches(cuda_ok):
+    page = 8
+    table = torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+    lt, rc = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda")
+    caches = [torch.zeros((0, page, 2, 64), dtype=BF, device="cuda") for _ in range(2)]
+    assert api.paged_compact(table, rc, caches).tolist() == [0]
+    assert api.paged_fork(table, lt, rc, _i32([0]), _i32([1]), page, caches).tolist() == [1]     # nothing of nothing
+    assert api.paged_extend(table, lt, rc, _i32([0, 2]), _i32([1, 0]), page).tolist() == [-1, 0]
+    api.check_device_status()
+    assert (table == -1).all() and (lt == 0).all()
