@@ -625,6 +625,20 @@ def _need_out(t, name: str, like, dtype, shape):
     return t
 
 
+def _scratch(workspace, like, need):
+    """The caller's workspace, or a new one of need() bytes beside `like`; (tensor, bytes).  One that the device cannot
+    reach is refused here: the library sees an address only."""
+    if workspace is None:
+        nbytes = need()
+        return like.new_empty(nbytes, dtype=torch.uint8), nbytes
+    if not isinstance(workspace, torch.Tensor) or workspace.device != like.device:
+        raise ValueError(f"workspace must be a tensor on {like.device}, got "
+                         f"{workspace.device if isinstance(workspace, torch.Tensor) else type(workspace).__name__}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
 def _ints(t, name: str, dev, n=None):
     """The length of a list int32 [n] on the device."""
     if t is None or t.dtype != torch.int32 or t.device != dev or t.dim() != 1 or not t.is_contiguous():
@@ -761,14 +775,10 @@ def paged_attn_decode(q, k_cache, v_cache, block_table, seq_lens, window: Option
     out = _need_out(out, "out", q, dt, qs)
     lse = _need_out(lse, "lse", q, torch.float32, qs[:-1])
     with _on_device(dev.index):
-        if workspace is None:
-            have = lib.sa_paged_attn_decode_workspace_size(B, Hq, Hkv, d)
-            workspace = q.new_empty(have, dtype=torch.uint8)
-        else:
-            have = workspace.numel() * workspace.element_size()
+        ws, have = _scratch(workspace, q, lambda: lib.sa_paged_attn_decode_workspace_size(B, Hq, Hkv, d))
         rc = lib.sa_paged_attn_decode(shape, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                       block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                      _ptr(workspace), have, _raw_stream(dev.index))
+                                      _ptr(ws), have, _raw_stream(dev.index))
     if rc:
         check(rc, "sa_paged_attn_decode")
     return out, lse
@@ -813,11 +823,9 @@ def _page_caches(what, caches, dev, n_pages, page):
     return struct.pack(f"={len(fields)}q", *fields), slot_bytes, page
 
 
-def _books_workspace(lib, S, n, n_pages, like, workspace):
-    if workspace is not None:
-        return workspace, workspace.numel() * workspace.element_size()
-    nbytes = lib.sa_paged_books_workspace_size(S, n, n_pages)
-    return like.new_empty(nbytes, dtype=torch.uint8), nbytes
+def paged_books_workspace_bytes(S, n, n_pages) -> int:
+    """Bytes that paged_extend and paged_fork of lists of n, and paged_compact (n = 0), need for tables of S rows."""
+    return int(_lib.load().sa_paged_books_workspace_size(S, n, n_pages))
 
 
 def paged_extend(block_table, seq_lens, refcount, seqs, n_new, page: int, start=None, workspace=None):
@@ -833,7 +841,7 @@ def paged_extend(block_table, seq_lens, refcount, seqs, n_new, page: int, start=
     _ints(n_new, "n_new", dev, n)
     start = _need_out(start, "start", seqs, torch.int32, (n,))
     with _on_device(dev.index):
-        ws, have = _books_workspace(lib, S, n, n_pages, refcount, workspace)
+        ws, have = _scratch(workspace, refcount, lambda: lib.sa_paged_books_workspace_size(S, n, n_pages))
         rc = lib.sa_paged_extend(block_table.data_ptr(), seq_lens.data_ptr(), refcount.data_ptr(), S, max_pages,
                                  n_pages, int(page), seqs.data_ptr(), n_new.data_ptr(), n, start.data_ptr(),
                                  _ptr(ws), have, _raw_stream(dev.index))
@@ -891,7 +899,7 @@ def paged_fork(block_table, seq_lens, refcount, src, dst, page: int, caches=(), 
     arr, slot_bytes, page = _page_caches("paged_fork", caches, dev, n_pages, int(page))
     done = _need_out(done, "done", src, torch.int32, (n,))
     with _on_device(dev.index):
-        ws, have = _books_workspace(lib, S, n, n_pages, refcount, workspace)
+        ws, have = _scratch(workspace, refcount, lambda: lib.sa_paged_books_workspace_size(S, n, n_pages))
         rc = lib.sa_paged_fork(block_table.data_ptr(), seq_lens.data_ptr(), refcount.data_ptr(), S, max_pages, n_pages,
                                page, src.data_ptr(), dst.data_ptr(), n, arr, len(caches), slot_bytes, done.data_ptr(),
                                _ptr(ws), have, _raw_stream(dev.index))
@@ -928,7 +936,7 @@ def paged_compact(block_table, refcount, caches=(), page: Optional[int] = None, 
     arr, slot_bytes, page = _page_caches("paged_compact", caches, dev, n_pages, page if caches else (page or 1))
     n_live = _need_out(n_live, "n_live", refcount, torch.int32, (1,))
     with _on_device(dev.index):
-        ws, have = _books_workspace(lib, S, 0, n_pages, refcount, workspace)
+        ws, have = _scratch(workspace, refcount, lambda: lib.sa_paged_books_workspace_size(S, 0, n_pages))
         rc = lib.sa_paged_compact(block_table.data_ptr(), refcount.data_ptr(), S, max_pages, n_pages, page, arr,
                                   len(caches), slot_bytes, n_live.data_ptr(), _ptr(ws), have, _raw_stream(dev.index))
     if rc:
