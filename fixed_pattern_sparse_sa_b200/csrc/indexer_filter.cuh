@@ -66,7 +66,7 @@ struct FtSmem {
     static constexpr int OFF_BAR = OFF_FAST + 16;
     // a_full[S], a_empty[S], b_full[2], b_empty[2], meta_full[2], meta_empty[2],
     // acc_full[2], acc_free[2], drain
-    static constexpr int N_BAR = 2 * FT_STAGES + 10 + 1;
+    static constexpr int N_BAR = 2 * FT_STAGES + 12 + 1;
     static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;      // tmem slot, abort flag
     static constexpr int TOTAL = OFF_MISC + 16;
     // at least ~116 KB so that one CTA (and its 512 TMEM columns) holds an SM

@@ -586,7 +586,7 @@ struct SkSmem {
     static constexpr int OFF_BAR = OFF_STAT + 4 * 64 * 8;
     // kv_full, kv_empty, q_full[S], q_empty[S], sd_full[2], pd_full[2], pd_done[2], acc_full, acc_free, drain[2],
     // item_full[2], item_empty[2], stat_full[2]
-    static constexpr int N_BAR = 16 + 2 * KVT_STAGES;
+    static constexpr int N_BAR = 18 + 2 * KVT_STAGES;
     static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;   // tmem slot, abort flag, -, -, unit info[S]
     static constexpr int OFF_ITEM = OFF_MISC + 32;
     static constexpr int TOTAL = OFF_ITEM + 2 * 64;
