@@ -61,7 +61,8 @@ class sa_sink_shape(ctypes.Structure):
                 [("scale", ctypes.c_float)] +
                 [(n, ctypes.c_int64) for n in ("Tq", "L", "q_pos0", "max_q", "max_k")] +
                 [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride", "dout_stride",
-                                                "lse_stride")])
+                                                "lse_stride")] +
+                [(n, ctypes.c_int32) for n in ("weight_parts", "reserved")])
 
 
 class sa_paged_shape(ctypes.Structure):

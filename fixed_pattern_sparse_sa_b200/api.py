@@ -542,7 +542,7 @@ def dsa_decode_workspace_bytes(B, Tq, L, Hq, d, Hi, di, topk, window=0, n_split=
 # than a careless binding on the host: the checks take a short way for tensors
 # as they should be, and the slow helpers only word the refusal.
 _ATTN_TYPES = {torch.bfloat16: _lib.SA_BF16, torch.float16: _lib.SA_FP16}
-_SINK_SHAPE = struct.Struct("=7if20q")             # sa_sink_shape
+_SINK_SHAPE = struct.Struct("=7if20q2i")           # sa_sink_shape
 _INT_MAX = 2 ** 31 - 1                              # a longer window sees no more
 _PAGED_SHAPE = struct.Struct("=9if9q")             # sa_paged_shape
 assert _SINK_SHAPE.size == ctypes.sizeof(_lib.sa_sink_shape)
@@ -686,17 +686,26 @@ def _sink_shape(what, q, k, v, window, sinks, cu_q, cu_k, max_q, max_k, scale, q
             Tq, L, pos0, max_q or 0, max_k or 0, *st), dev, packed
 
 
+def _parts(weight_parts) -> int:
+    if weight_parts not in (None, 1, 2):
+        raise ValueError(f"weight_parts must be 1, 2 or None (by the size of the call), got {weight_parts}")
+    return weight_parts or 0
+
+
 def sink_attn_fwd(q, k, v, window: int, sinks: int = 0, cu_q=None, cu_k=None, max_q: Optional[int] = None,
                   max_k: Optional[int] = None, scale: Optional[float] = None, q_pos0: Optional[int] = None,
-                  out=None, lse=None):
+                  out=None, lse=None, weight_parts: Optional[int] = None):
     """Causal attention over a sliding window plus the first `sinks` keys (sa_sink_attn_fwd).
 
     Dense: q bf16 or fp16 [B,Tq,Hq,d], k/v [B,L,Hkv,d]; q_pos0 defaults to
     L - Tq.  Packed: q [N,Hq,d], k/v [M,Hkv,d] with cu_q, cu_k int32 [B+1] (a
     sequence's last query stands at its last key) and max_q, max_k, upper
     bounds of the lengths.  q, k and v may be strided views (the parts of one
-    projection).  Returns (out like q, contiguous, lse fp32 [..., Hq]); rows
-    outside every packed sequence are left as they were in `out` and `lse`.
+    projection).  weight_parts: 1 or 2, how exactly the weights enter the
+    second product (None: 2 up to 8192 rows of q, 1 above; a fixed number
+    makes a sequence's results independent of the batch).  Returns (out like
+    q, contiguous, lse fp32 [..., Hq]); rows outside every packed sequence are
+    left as they were in `out` and `lse`.
     """
     lib = _lib.load()
     f, dev, packed = _sink_shape("sink_attn_fwd", q, k, v, window, sinks, cu_q, cu_k, max_q, max_k, scale, q_pos0,
@@ -705,8 +714,9 @@ def sink_attn_fwd(q, k, v, window: int, sinks: int = 0, cu_q=None, cu_k=None, ma
     out = _need_out(out, "out", q, q.dtype, qs)
     lse = _need_out(lse, "lse", q, torch.float32, qs[:-1])
     with _on_device(dev.index):
-        rc = lib.sa_sink_attn_fwd(_SINK_SHAPE.pack(*f, 0, 0, 0, 0, 0, 0), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                  _ptr(cu_q), _ptr(cu_k), out.data_ptr(), lse.data_ptr(), _raw_stream(dev.index))
+        rc = lib.sa_sink_attn_fwd(_SINK_SHAPE.pack(*f, 0, 0, 0, 0, 0, 0, _parts(weight_parts), 0), q.data_ptr(),
+                                  k.data_ptr(), v.data_ptr(), _ptr(cu_q), _ptr(cu_k), out.data_ptr(), lse.data_ptr(),
+                                  _raw_stream(dev.index))
     if rc:
         check(rc, "sa_sink_attn_fwd")
     return out, lse
@@ -714,7 +724,7 @@ def sink_attn_fwd(q, k, v, window: int, sinks: int = 0, cu_q=None, cu_k=None, ma
 
 def sink_attn_bwd(q, k, v, out, lse, dout, window: int, sinks: int = 0, cu_q=None, cu_k=None,
                   max_q: Optional[int] = None, max_k: Optional[int] = None, scale: Optional[float] = None,
-                  q_pos0: Optional[int] = None, dq=None, dk=None, dv=None):
+                  q_pos0: Optional[int] = None, dq=None, dk=None, dv=None, weight_parts: Optional[int] = None):
     """Backward of sink_attn_fwd (sa_sink_attn_bwd), bf16.
 
     out and lse are the forward's (out may be None: only lse is read); the
@@ -730,7 +740,8 @@ def sink_attn_bwd(q, k, v, out, lse, dout, window: int, sinks: int = 0, cu_q=Non
         _rows(out, "out", bf, dev, qs)
     if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or lse.device != dev or lse.shape != qs[:-1]:
         raise ValueError("sink_attn_bwd: lse must be the forward's, fp32 and shaped like q without d")
-    shape = _SINK_SHAPE.pack(*f, *lead, *_rows(dout, "dout", bf, dev, qs), *lead, *lse.stride())
+    shape = _SINK_SHAPE.pack(*f, *lead, *_rows(dout, "dout", bf, dev, qs), *lead, *lse.stride(),
+                             _parts(weight_parts), 0)
     dq, dk, dv = _need_out(dq, "dq", q, bf, qs), _need_out(dk, "dk", k, bf, k.shape), _need_out(dv, "dv", v, bf, v.shape)
     with _on_device(dev.index):
         nbytes = lib.sa_sink_attn_bwd_workspace_size(shape, int(packed))

@@ -37,6 +37,8 @@ static int sink_check(const char *what, const sa_sink_shape *s, const void *q, c
         return fail(SA_ERR_INVALID_ARG, "%s: bad sizes (Hq a multiple of Hkv)", what);
     if (s->window < 1 || s->sinks < 0) return fail(SA_ERR_INVALID_ARG, "%s: window >= 1, sinks >= 0", what);
     if (!std::isfinite(s->scale) || s->scale <= 0.f) return fail(SA_ERR_INVALID_ARG, "%s: scale must be positive", what);
+    if (s->weight_parts < 0 || s->weight_parts > 2)
+        return fail(SA_ERR_INVALID_ARG, "%s: weight_parts %d (0, 1 or 2)", what, s->weight_parts);
     if (s->d != 64 && s->d != 128) return fail(SA_ERR_UNSUPPORTED, "%s: head dim %d (64 or 128)", what, s->d);
     if (s->dtype != SA_BF16 && (bwd || s->dtype != SA_FP16))
         return fail(SA_ERR_UNSUPPORTED, "%s: dtype %d", what, s->dtype);
@@ -110,13 +112,20 @@ static int rows_tensor_map(CUtensorMap *m, const void *base, int d, long long he
     return SA_OK;
 }
 
-// Calls of few rows take their weights in two parts (SPLIT).  There the
-// rounding of the weights does not average out: gradients of 36 rows were 1.9
-// times as far from 64 bits as their own rounding, of some hundred rows up to
-// 1.5 times, of many thousand 1.42 times.  And there it costs little: a
-// forward of 2048 rows 16.0 us either way; where the products bind it does
-// not pay (64K forward 1.24 -> 2.2 ms, backward of 16000 rows 28 -> 33 us).
-static bool sink_split(const SinkParams &p) {
+// Weights in two parts (SPLIT) or one.  Measured over 1500 rows, in output
+// roundings: one part 1.07 (two visible keys) to 1.40 (1024) in out, 1.40 to
+// 1.43 in the gradients, single rows up to 3.5; two parts 1.00 throughout.
+// The number of keys seen does not decide it, the number of rows that the
+// caller sees does: 36 rows came out at 1.9.  Two parts cost, one -> two in us
+// (window 512 unless named):
+//   forward   2048 rows (window 32) 8.4 -> 8.5, 8192 rows 14.7 -> 24.2,
+//             65536 rows 31 -> 51, 64K x 16 heads (window 2048) 1083 -> 2182
+//   backward  2048 rows (window 32) 25 -> 31, 8192 rows 137 -> 229,
+//             16K x 64 heads 1862 -> 2390, 64K x 16 heads (2048) 5958 -> 7535
+// So the caller chooses; left open, calls of up to 8192 rows take two (there
+// 0.01 ms more in a forward, 0.09 ms in a backward).
+static bool sink_split(const sa_sink_shape *s, const SinkParams &p) {
+    if (s->weight_parts) return s->weight_parts == 2;
     return (p.cu_q ? 1 : p.B) * p.Tq * p.Hq <= 8192;
 }
 
@@ -176,7 +185,7 @@ extern "C" int sa_sink_attn_fwd(const sa_sink_shape *shape, const void *q, const
     using B = __nv_bfloat16;
     using H = __half;
     const bool bf = shape->dtype == SA_BF16;
-    if (sink_split(p))
+    if (sink_split(shape, p))
         return shape->d == 64 ? (bf ? sink_fwd_launch<B, 64, true>(p, st) : sink_fwd_launch<H, 64, true>(p, st))
                               : (bf ? sink_fwd_launch<B, 128, true>(p, st) : sink_fwd_launch<H, 128, true>(p, st));
     return shape->d == 64 ? (bf ? sink_fwd_launch<B, 64, false>(p, st) : sink_fwd_launch<H, 64, false>(p, st))
@@ -307,7 +316,7 @@ extern "C" int sa_sink_attn_bwd(const sa_sink_shape *shape, const void *q, const
     p.dq = dq; p.dk = dk; p.dv = dv; p.stat = static_cast<float2 *>(workspace);
     if (shape->Tq == 0 && shape->L == 0) return SA_OK;
     cudaStream_t st = as_stream(stream);
-    if (sink_split(p))
+    if (sink_split(shape, p))
         return shape->d == 64 ? sink_bwd_launch<64, true>(p, workspace, st) : sink_bwd_launch<128, true>(p, workspace, st);
     return shape->d == 64 ? sink_bwd_launch<64, false>(p, workspace, st) : sink_bwd_launch<128, false>(p, workspace, st);
 }

@@ -402,6 +402,18 @@ int sa_index_shard(const int32_t *idx, int64_t n, int64_t key_lo, int64_t key_hi
  * not reach a forward row, infinities and NaN included; the backward wants
  * finite inputs within a sequence (what lies outside every sequence, or
  * behind the last visible key, may hold anything).
+ *
+ * weight_parts: the weights P, and dS in the backward, enter their second
+ * products in the inputs' type.  1: rounded to it.  2: what the rounding
+ * leaves enters as well (2^-16 of a weight).  With 1 an output is 1.1 to 1.4
+ * times, a gradient 1.4 times as far from its exact value as rounding it
+ * makes it (2-norm over 1500 rows of 2 to 1024 visible keys; single rows up
+ * to 3.5 times), with 2 it is 1.0 times.  2 costs up to 2 times the forward's
+ * and 1.2 to 1.9 times the backward's time.  0: 2 in calls of up to 8192 rows
+ * (queries of the batch x Hq), where a caller sees few rows and thus the
+ * single row's error, and 1 above; a sequence's results then change with the
+ * size of the batch, which 1 or 2 avoids (the order of the sinks' sums in dk
+ * and dv still follows the batch).
  * ------------------------------------------------------------------------ */
 enum sa_dtype { SA_BF16 = 0, SA_FP16 = 1 };
 
@@ -415,6 +427,8 @@ typedef struct sa_sink_shape {
     int64_t max_q, max_k;       /* packed only: upper bounds of the lengths, 0 = not known */
     int64_t q_stride[3], k_stride[3], v_stride[3];                  /* batch, token, head */
     int64_t dout_stride[3], lse_stride[3];                          /* backward only */
+    int32_t weight_parts;       /* 1 or 2; 0: by the size of the call */
+    int32_t reserved;
 } sa_sink_shape;
 
 int sa_sink_attn_fwd(const sa_sink_shape *shape, const void *q, const void *k, const void *v, const int32_t *cu_q,
