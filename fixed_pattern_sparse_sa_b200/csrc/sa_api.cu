@@ -30,7 +30,6 @@
 #include "nsa_bwd_tc.cuh"
 #include "probe_gather.cuh"
 
-
 using namespace sa;
 
 // ------------------------------------------------------------- error state --

@@ -212,7 +212,7 @@ static SinkKvTiles sink_kv_tiles(const SinkParams &p) {
     t.tps = (int)std::max<long long>(nq, 1);
     if (t.n_kt && nq) {
         const long long want = std::max({(4ll * t.TPT + t.HC - 1) / t.HC, (p.window + 131ll) / 4, (nq + 63) / 64});
-        const long long most = std::max<long long>(1, 4ll * 148 / ((long long)p.B * p.Hkv * t.n_kt));
+        const long long most = std::max<long long>(1, 4ll * sm_count() / ((long long)p.B * p.Hkv * t.n_kt));
         t.n_split = (int)std::min(most, (nq + want - 1) / want);
         t.tps = (int)((nq + t.n_split - 1) / t.n_split);
     }
