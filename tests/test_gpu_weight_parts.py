@@ -9,7 +9,7 @@ import torch
 
 import _sink_ref as ref
 import _tight_ref as tight
-from fixed_pattern_sparse_sa_b200 import api
+from fixed_pattern_sparse_sa_b200 import _lib, api
 from test_gpu_sink_attn import BF, DENSE, HF, _dense, _packed, _rand
 from test_gpu_sink_attn import PACKED as SMALL_PACKED
 from test_gpu_sink_large import LARGE
@@ -136,3 +136,31 @@ def test_refusals(cuda_ok):
     with pytest.raises(ValueError, match="weight_parts"):
         api.sink_attn_bwd(q, k, v, out, lse, q, 4, weight_parts=3)
     assert torch.equal(out, api.sink_attn_fwd(q, k, v, 4, weight_parts=2)[0])
+
+
+@pytest.mark.parametrize("parts", [1, 2])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_wait_that_runs_out_is_reported(cuda_ok, d, parts):
+    # the stall hook keeps the kernels from loading anything: their first waits run out after the spin limit
+    q, k, v = _dense(1, 1100, 1100, 8, 2, d, BF, 71)
+    dout = torch.randn(q.shape, device="cuda").to(BF)
+
+    def step():
+        out, lse = api.sink_attn_fwd(q, k, v, 100, 20, weight_parts=parts)
+        return out, lse, *api.sink_attn_bwd(q, k, v, None, lse, dout, 100, 20, weight_parts=parts)
+
+    want = step()
+    api.check_device_status()
+    try:
+        api.debug_set_spin_limit(20_000_000)                      # about 10 ms
+        api.debug_inject_stall(True)
+        step()
+        with pytest.raises(api.SAError) as e:
+            api.check_device_status()
+        assert e.value.status == _lib.SA_ERR_TIMEOUT
+    finally:
+        api.debug_inject_stall(False)
+        api.debug_set_spin_limit(0)
+    got = step()
+    api.check_device_status()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
