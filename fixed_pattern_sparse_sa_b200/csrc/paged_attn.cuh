@@ -24,9 +24,9 @@
 // parts are above 0, so an infinity in a visible V stays one (0 * inf, or
 // parts of different signs, would make it NaN).  All sums are fp32.
 //
-// Measured on one B200: 32 sequences of 128K, 16 heads on one KV head, 378 us =
-// 5.7 TB/s (87 % of a copy's rate); 192 ragged sequences, window 4096 and 64
-// sinks, 64 heads on 8, 349 us = 5.2 TB/s.
+// Measured on one B200: 32 sequences of 128K, 16 heads on one KV head, 386 us =
+// 5.6 TB/s (85 % of a copy's rate; 358 us on another); 192 ragged sequences,
+// window 4096 and 64 sinks, 64 heads on 8, 353 us = 5.1 TB/s.
 #pragma once
 
 #include "sa_common.cuh"

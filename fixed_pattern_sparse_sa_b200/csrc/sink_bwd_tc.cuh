@@ -11,16 +11,17 @@
 // Two passes, each with its sums in tensor memory from first to last, so
 // nothing is added up in global memory and the result does not depend on the
 // order of the blocks: query-major for dq, key-major for dk and dv.  The
-// price is that S and dP are formed twice (7 products instead of 5); adding
-// dq up from the key-major pass would move 4 bytes per element of dq and key
-// tile through L2 atomics instead, in varying order.
+// price is that S and dP are formed three times (9 products instead of 5): in
+// the query-major pass once for D and once for dq, and in the key-major one;
+// adding dq up from the key-major pass would move 4 bytes per element of dq
+// and key tile through L2 atomics instead, in varying order.
 //
 // P and dS are rounded to bf16 for the second products (with SPLIT what that
 // leaves enters as another product); sums are fp32 and rounded once.
 //
 // Measured on one B200: 16K tokens, 64 heads on 4 KV heads, window 512, 16
-// sinks 1.90 ms = 367 TFLOP/s of the formulas' 10 d flops a pair (dq 1.0 ms,
-// dk and dv 0.8 ms, 990 W at 1660 MHz); 2 x 1000 tokens, 8 heads, 28 us.
+// sinks 1.94 ms = 359 TFLOP/s of the formulas' 10 d flops a pair (dq 1.0 ms,
+// dk and dv 0.8 ms, 990 W at 1660 MHz); 2 x 1000 tokens, 8 heads, 29 us.
 #pragma once
 
 #include "sink_fwd_tc.cuh"

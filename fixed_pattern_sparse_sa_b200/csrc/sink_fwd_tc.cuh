@@ -35,8 +35,8 @@
 // producer, 9 and 10 MMA issuers of A and B (9 also owns the TMEM).
 //
 // Measured on one B200: 64K tokens, 16 heads on one KV head, window 2048, 128
-// sinks 1.24 ms = 928 TFLOP/s (990 W, 1860 MHz); 7 ragged fp16 prompts, 8000
-// tokens, 16 heads on 4, window 512, 72 us = 405 TFLOP/s.  Every wait is bounded; a timeout
+// sinks 1.23 ms = 933 TFLOP/s (990 W, 1860 MHz); 7 ragged fp16 prompts, 8000
+// tokens, 16 heads on 4, window 512, 73 us = 403 TFLOP/s.  Every wait is bounded; a timeout
 // sets ERR_TIMEOUT and the CTA drains and exits.
 #pragma once
 

@@ -387,8 +387,8 @@ int sa_index_shard(const int32_t *idx, int64_t n, int64_t key_lo, int64_t key_hi
  * or leaves [0, rows], or a length above its bound, sets the device error
  * word; what is cut off by that sequence's clamped ends is left as it was.
  *
- * dtype: bf16 or fp16 in the forward, bf16 in the backward (without a loss
- * scale dS falls below fp16's normal range).  q, k, v and dout are strided:
+ * dtype: bf16 or fp16 in the forward; the backward takes bf16 alone.  q, k, v
+ * and dout are strided:
  * *_stride gives the elements between batches, tokens and heads (packed: the
  * batch stride is not used); the last dimension is contiguous, every stride a
  * multiple of 8 elements and not 0 over more than one step (no broadcast
@@ -510,7 +510,8 @@ int sa_paged_attn_decode(const sa_paged_shape *shape, const void *q, const void 
  *   copied in each of the n_caches caches to a fresh page, taken as in
  *   sa_paged_extend; -1 entries stay -1.  done[i] = 1, or 0 where no page was
  *   left or the entry is wrong (src or dst outside the table, dst listed
- *   twice (its first place counts), dst that is also a src, dst in use).
+ *   twice (its first place counts), dst that is also a src, dst in use, a row
+ *   of src that names a page outside the pool or lacks its partly filled one).
  * sa_paged_free: window = 0: the pages of seqs[i] are given back (refcount -
  *   1), its table row becomes -1, its length 0.  window > 0: only the pages
  *   that no later query can see are given back, those whose positions are all
